@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8w8a8.so")
-SOURCES = ["abi.hip", "quant_kernels.hip", "gemm_kernels.hip", "kv_kernels.hip"]
+SOURCES = ["abi.hip", "quant_kernels.hip", "gemm_kernels.hip", "kv_kernels.hip",
+           "attention_abi.hip", "slot_kernels.hip", "rope_kernels.hip", "attention_kernels.hip"]
 PROBE_SOURCE = "hbm_probe.hip"                 # bench.py's HBM and matrix-unit references
 PROBE_LIB = os.path.join(PKG, "libhbmprobe.so")
 ARCH = "gfx950"

@@ -3,37 +3,12 @@
 // checks of "[vLLM] FP8", block quantization (block mode needs pre-quantized
 // weights, a two-dimensional block size, and a dynamic activation scheme),
 // turned into status codes returned before anything is enqueued.
-#include <atomic>
-#include <cstring>
-
-#include "fp8w8a8.h"
+#include "abi_common.h"
 #include "launch.h"
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t)1 << 31;        // any single extent
-constexpr int64_t kMaxElems = (int64_t)1 << 40;      // rows * cols of one tensor
-constexpr int64_t kMaxSpan = (int64_t)1 << 56;       // rows * ld of one tensor (elements)
-
-// rows rows at leading dimension ld span at most kMaxSpan elements, so every
-// byte range below is computed without overflow
-bool span_ok(int64_t rows, int64_t ld) {
-  return ld >= 0 && ld <= kMaxSpan && (rows <= 1 || ld <= kMaxSpan / rows);
-}
-
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-// Byte range [lo, hi) of a row-major matrix.
-struct Range {
-  uintptr_t lo, hi;
-};
-Range range_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
-  uintptr_t lo = (uintptr_t)p;
-  if (rows <= 0 || cols <= 0) return {lo, lo};
-  uintptr_t hi = lo + (uintptr_t)(((rows - 1) * ld + cols) * elem);
-  return {lo, hi};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+using namespace fp8abi;
 
 bool shape_ok_kn(int64_t K) { return K > 0 && K % 128 == 0 && K < kMaxDim; }
 
@@ -127,25 +102,6 @@ fp8_status validate_gemm(const uint8_t* a_q, int64_t ld_a, const float* a_s, int
   if (overlap(ro, ra) || overlap(ro, rw) || overlap(ro, ras) || overlap(ro, rws)) return FP8_ERR_ALIAS;
   return FP8_OK;
 }
-
-// Per-device cache of "is this a gfx950": 0 unknown, 1 yes, 2 no.
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_arch_ok[kMaxDevices];
-
-fp8_status check_device() {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return FP8_ERR_DEVICE;
-  int state = g_arch_ok[dev].load(std::memory_order_relaxed);
-  if (state == 0) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return FP8_ERR_DEVICE;
-    state = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-    g_arch_ok[dev].store(state, std::memory_order_relaxed);
-  }
-  return state == 1 ? FP8_OK : FP8_ERR_DEVICE;
-}
-
-fp8_status launched(hipError_t e) { return e == hipSuccess ? FP8_OK : FP8_ERR_LAUNCH; }
 
 // Workspace of the unfused fp8_linear path: activation codes [M, ld = K
 // rounded up to 16], then the scales (block: [M, K/128]; row: [M]; tensor:

@@ -1,0 +1,1338 @@
+// Attention over the paged FP8 cache for gfx950: ragged batches, causal, with
+// an optional sliding window and sinks, and batches behind a shared prefix.
+//
+// For a query row q at position p of its request (one row per query head):
+//   s_j = scale * k_scale * <q, dec(K_j)>,  out = v_scale * sum_j softmax(s)_j dec(V_j)
+// over the visible j.  One pass over the keys keeps a running maximum m, the
+// sum l = sum exp(s_j - m) and O = sum exp(s_j - m) V_j, rescaled when m grows.
+//
+// Numbers.  E4M3 codes convert exactly to bf16 and to fp16 (4 significant
+// bits, 2^-9 .. 448), queries are bf16, so <q, K_j> is a sum of exact products
+// on the bf16 matrix instruction with fp32 accumulation, and nothing of the
+// scores is rounded below fp32.  P = exp(s - m) <= 1 goes to fp16, whose 11
+// bits keep its rounding (2^-11 relative, 2^-25 absolute below 2^-14) an order
+// under the bf16 output's; O is fp32, and l sums the fp32 values.  exp(x) is
+// exp2(x log2 e), the factor folded into the score scale.
+//
+// Layout.  S^T = K Q^T puts one query row in each lane column, so m, l and the
+// rescaling of O^T = V^T P^T stay in the lane's own column, and P's registers
+// are the second product's operand as they are: the matrix instruction sums
+// over its k index in any order, so the keys of a lane's P values (rows of the
+// S^T tile it holds) are simply the keys whose V bytes it is given.
+//
+// Rows.  The G = Hq / Hk query heads of a KV head share its keys: row rho of
+// request r and KV head h is token rho / G, head h G + rho % G.
+//
+// Work.  An item is (request, row tile, KV head); its cost is the number of
+// key tiles its mask leaves.  A fixed grid of workgroups takes even shares of
+// the whole list's tiles, found by a prefix sum over the requests that every
+// workgroup forms itself, so no length is needed on the host and ragged
+// batches, one long context and many short ones all fill the card.  An item
+// inside one share is finished there; one that shares cut leaves fp32 partial
+// rows (O, m, l) in the workspace, and a second launch joins them.
+#include <atomic>
+
+#include "attention_launch.h"
+#include "device_common.h"
+#include "launch.h"
+
+namespace fp8k {
+
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+#define FP8_NEG_INF (-__builtin_inff())
+
+// ---- workspace -----------------------------------------------------------------
+// descriptor of an item that starts in a workgroup's share and ends in a later one
+struct Split {
+  int32_t token0;      // the request's first token
+  int32_t row0, rows;  // rows of the tile
+  int32_t head;        // KV head
+  int32_t parts;       // workgroups that hold a part of it (0: none starts here)
+  int32_t pad[3];
+};
+
+// partial rows of a launch: workgroup w writes slot 2 w (an item that began
+// before its share) and slot 2 w + 1 (one that goes on behind it)
+struct Parts {
+  float* ml;           // [slots][R][2]: m (of the scores times log2 e) and l
+  float* o;            // [slots][R][D]
+  Split* split;        // [workgroups]
+  // shared prefix only: where each row's result is, and rows that one
+  // workgroup finished
+  int2* where;         // [T * Hq]: row of ml / o of the first part, number of parts
+                       // (0: in whole_*; < 0: a row of no request)
+  int2* reset;         // where[] of the launch behind this one, set to "of no request"
+  float* whole_ml;     // [T * Hq][2]
+  float* whole_o;      // [T * Hq][D]
+};
+
+// ---- which keys a row tile needs ------------------------------------------------
+struct Request {
+  int token0, n;       // first query token, query tokens
+  int p0;              // position of the first one
+  int keys;            // keys that the table can hold and the length names
+};
+
+// keys of a request: key indices of its last tile stay below 2^31
+__device__ __forceinline__ int keys_of(const AttentionArgs& a, int len, int32_t width) {
+  int64_t cap = a.num_blocks > 0 ? (int64_t)width * a.page : 0;
+  cap = cap < 0x7fffff00ll ? cap : 0x7fffff00ll;
+  return len < 0 ? 0 : (int64_t)len < cap ? len : (int)cap;
+}
+
+struct Tiles {
+  int sink;            // tiles 0 .. sink - 1, then
+  int first, last;     // tiles first .. last - 1
+  int p_lo, p_hi;      // positions of the tile's first and last token
+  __device__ __forceinline__ int count() const { return sink + last - first; }
+  __device__ __forceinline__ int key_tile(int k) const { return k < sink ? k : first + k - sink; }
+};
+
+// kPrefix: the rows are all T tokens and see all of the prefix.
+template <bool kPrefix>
+__device__ __forceinline__ Request load_request(const AttentionArgs& a, int r) {
+  Request q;
+  if (kPrefix) {
+    q.token0 = 0;
+    q.n = a.T;
+    q.keys = keys_of(a, a.prefix_len[0], a.prefix_width);
+    q.p0 = q.keys - 1;
+  } else {
+    int lo = a.offsets[r], hi = a.offsets[r + 1];
+    lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
+    hi = hi < lo ? lo : hi > a.T ? a.T : hi;
+    const int len = a.lens[r] > 0 ? a.lens[r] : 0;
+    q.token0 = lo;
+    q.n = hi - lo;
+    q.p0 = len - q.n;
+    q.keys = keys_of(a, len, a.width);
+  }
+  return q;
+}
+
+__device__ __forceinline__ int row_tiles(const AttentionArgs& a, const Request& q, int R) {
+  return (int)(((int64_t)q.n * a.G + R - 1) / R);
+}
+
+template <bool kPrefix, int R, int KT>
+__device__ __forceinline__ Tiles tiles_of(const AttentionArgs& a, const Request& q, int m) {
+  Tiles t;
+  if (kPrefix) {
+    t.p_lo = t.p_hi = q.keys - 1;
+    t.sink = t.first = 0;
+    t.last = (q.keys + KT - 1) / KT;
+    return t;
+  }
+  const int64_t row = (int64_t)m * R;
+  const int i_lo = (int)(row / a.G);
+  const int64_t i_end = (row + R - 1) / a.G;
+  const int i_hi = i_end < q.n - 1 ? (int)i_end : q.n - 1;
+  t.p_lo = q.p0 + i_lo;
+  t.p_hi = q.p0 + i_hi;
+  const int hi = t.p_hi + 1 < q.keys ? t.p_hi + 1 : q.keys;
+  if (hi <= 0) {
+    t.sink = t.first = t.last = 0;
+    return t;
+  }
+  t.last = (int)(((int64_t)hi + KT - 1) / KT);
+  const int low = a.window > 0 && t.p_lo >= a.window ? t.p_lo - a.window + 1 : 0;
+  t.first = low / KT < t.last ? low / KT : t.last;
+  const int sink_end = a.sinks < hi ? a.sinks : hi;
+  const int st = (int)(((int64_t)sink_end + KT - 1) / KT);
+  t.sink = st < t.first ? st : t.first;
+  return t;
+}
+
+// cost of a row tile: its key tiles, one at least (its rows are written)
+__device__ __forceinline__ int cost_of(const Tiles& t) {
+  const int c = t.count();
+  return c > 1 ? c : 1;
+}
+
+// ---- shares ----------------------------------------------------------------------
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// exclusive prefix of v over the workgroup; total in `all`
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_wave, int64_t& all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t u = __shfl_up(x, d);
+    if (lane >= d) x += u;
+  }
+  __syncthreads();
+  if (lane == 63) s_wave[wave] = x;
+  __syncthreads();
+  int64_t before = 0;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) {
+    if (w < wave) before += s_wave[w];
+    all += s_wave[w];
+  }
+  return before + x - v;
+}
+
+template <bool kPrefix, int R, int KT>
+__device__ __forceinline__ int64_t request_cost(const AttentionArgs& a, int r) {
+  const Request q = load_request<kPrefix>(a, r);
+  const int mt = row_tiles(a, q, R);
+  int64_t c = 0;
+  if (kPrefix) {
+    if (mt > 0) c = (int64_t)mt * cost_of(tiles_of<kPrefix, R, KT>(a, q, 0));
+  } else {
+    for (int m = 0; m < mt; ++m) c += cost_of(tiles_of<kPrefix, R, KT>(a, q, m));
+  }
+  return c * a.Hk;
+}
+
+struct Place {
+  int64_t share, pos, end;   // tiles per workgroup, this one's range
+  int r, m, h, k;            // where pos is
+};
+
+// Finds this workgroup's share and where it begins.
+template <bool kPrefix, int R, int KT>
+__device__ __forceinline__ Place find_share(const AttentionArgs& a, int wg, int wgs,
+                                            int64_t* s_wave, int64_t* s_found) {
+  const int tid = threadIdx.x;
+  const int B = kPrefix ? 1 : a.B;
+  Place p;
+  int64_t total = 0;
+  // with at most one request per thread the first pass's scan is kept
+  int64_t first_cost = 0, first_before = 0;
+  for (int r0 = 0; r0 < B; r0 += kThreads) {
+    const int r = r0 + tid;
+    const int64_t c = r < B ? request_cost<kPrefix, R, KT>(a, r) : 0;
+    int64_t all;
+    const int64_t before = block_scan(c, s_wave, all);
+    if (r0 == 0) {
+      first_cost = c;
+      first_before = before;
+    }
+    total += all;
+  }
+  p.share = (total + wgs - 1) / wgs;
+  p.pos = p.share * wg;
+  p.end = p.pos + p.share < total ? p.pos + p.share : total;
+  p.r = p.m = p.h = p.k = 0;
+  if (p.pos >= p.end) return p;
+  int64_t base = 0;
+  for (int r0 = 0; r0 < B; r0 += kThreads) {
+    const int r = r0 + tid;
+    int64_t c = first_cost, before = first_before, all = total;
+    if (B > kThreads) {
+      c = r < B ? request_cost<kPrefix, R, KT>(a, r) : 0;
+      before = block_scan(c, s_wave, all);
+    }
+    const int64_t x = p.pos - base - before;
+    if (x >= 0 && x < c) {          // one thread of one pass
+      s_found[0] = r;
+      s_found[1] = x;
+    }
+    base += all;
+    if (p.pos < base) break;        // uniform
+  }
+  __syncthreads();
+  p.r = uniform((int)s_found[0]);
+  int64_t x = s_found[1];
+  const Request q = load_request<kPrefix>(a, p.r);
+  if (kPrefix) {
+    const int64_t c = cost_of(tiles_of<kPrefix, R, KT>(a, q, 0));
+    p.m = uniform((int)(x / (c * a.Hk)));
+    x -= (int64_t)p.m * c * a.Hk;
+    p.h = uniform((int)(x / c));
+    p.k = uniform((int)(x - p.h * c));
+    return p;
+  }
+  for (int m = 0;; ++m) {
+    const int64_t c = cost_of(tiles_of<kPrefix, R, KT>(a, q, m));
+    if (x < c * a.Hk) {
+      p.m = uniform(m);
+      p.h = uniform((int)(x / c));
+      p.k = uniform((int)(x - p.h * c));
+      return p;
+    }
+    x -= c * a.Hk;
+  }
+}
+
+// ---- paging ----------------------------------------------------------------------
+// Cache slot of key j of a request, -1 where no block is mapped.
+__device__ __forceinline__ int slot_of(const int32_t* table, int j, int keys, int page,
+                                       int num_blocks) {
+  if (j >= keys) return -1;
+  const int i = (int)((uint32_t)j / (uint32_t)page);
+  const int b = table[i];
+  return b >= 0 && b < num_blocks ? b * page + (j - i * page) : -1;
+}
+
+// ---- conversions -----------------------------------------------------------------
+__device__ __forceinline__ bf16x8 bf16_of_codes(uint32_t w0, uint32_t w1) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+__device__ __forceinline__ f16x8 f16_of_codes(uint32_t w0, uint32_t w1) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, false);
+  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, true);
+  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, false);
+  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, true);
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Bytes of four dwords transposed: o[b] holds byte b of w0 .. w3.
+__device__ __forceinline__ void transpose4(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3,
+                                           uint32_t o[4]) {
+  const uint32_t lo01 = __builtin_amdgcn_perm(w1, w0, 0x05010400u);  // a0 b0 a1 b1
+  const uint32_t hi01 = __builtin_amdgcn_perm(w1, w0, 0x07030602u);  // a2 b2 a3 b3
+  const uint32_t lo23 = __builtin_amdgcn_perm(w3, w2, 0x05010400u);
+  const uint32_t hi23 = __builtin_amdgcn_perm(w3, w2, 0x07030602u);
+  o[0] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
+  o[1] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
+}
+
+// nonzero iff one of the four codes is a NaN (S.1111.111)
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+__device__ __forceinline__ uint32_t bf16_rne(float f) {
+  return f != f ? 0x7fc0u : f32_to_bf16_rne(f);
+}
+
+__device__ __forceinline__ float max_xor32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_xor16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_xor32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float sum_xor16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// the maximum that exponents are taken against: rows that have seen no key
+// (m = -inf) take 0, so that exp2(-inf - 0) = 0 and nothing turns NaN
+__device__ __forceinline__ float base_of(float m) { return m == FP8_NEG_INF ? 0.0f : m; }
+
+// whether a row at position p sees key j (of a mapped page)
+__device__ __forceinline__ bool sees(int j, int p, int window, int sinks) {
+  return j <= p && (window == 0 || p - j < window || j < sinks);
+}
+
+// Arguments read again from the kernel's argument segment: what only an item's
+// end needs does not stay in scalar registers through its loop.
+struct KernelArgs {
+  AttentionArgs a;
+  Parts parts;
+};
+__device__ __forceinline__ const KernelArgs* fresh_args() {
+  uint64_t p = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return (const KernelArgs*)p;
+}
+
+// score factor and query sign: queries are negated (exactly) where the factor
+// is negative, so that the largest score is the largest product; a factor of 0
+// becomes one whose products vanish beside any maximum
+struct Factor {
+  float c;
+  uint32_t flip;                 // xor mask of two bf16 queries
+};
+__device__ __forceinline__ Factor factor_of(const AttentionArgs& a) {
+  const float c = a.scale * a.k_scale[0] * kLog2e;
+  Factor f;
+  f.c = c == 0.0f ? 0x1p-126f : __builtin_fabsf(c);
+  f.flip = c < 0.0f ? 0x80008000u : 0u;
+  return f;
+}
+
+__device__ __forceinline__ bf16x8 load_query(const uint16_t* p, uint32_t flip) {
+  const uint4 x = *reinterpret_cast<const uint4*>(p);
+  return __builtin_bit_cast(bf16x8, make_uint4(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip));
+}
+
+// NaN codes of a row of D values as bits: bit e of word w is value 32 w + e
+template <int kWords>
+struct NanBits {
+  uint32_t w[kWords];
+};
+
+// adds the NaN codes among 32 kWords bytes at p
+template <int kWords>
+__device__ __forceinline__ void add_nans(NanBits<kWords>& bits, const uint8_t* p) {
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    uint32_t got = 0u;
+#pragma unroll 1
+    for (int i = 7; i >= 0; --i) {
+      const uint32_t x = nan_codes(*reinterpret_cast<const uint32_t*>(p + 32 * w + 4 * i)) >> 7;
+      // bits 0, 8, 16, 24 together
+      got = got << 4 | ((x | x >> 7 | x >> 14 | x >> 21) & 0xfu);
+    }
+    bits.w[w] |= got;
+  }
+}
+
+// bytes of w that are NaN codes, cleared
+__device__ __forceinline__ uint32_t without_nans(uint32_t w) {
+  return w & ~((nan_codes(w) >> 7) * 0xffu);
+}
+
+// Where a workgroup's results of an item go.
+struct Target {
+  bool whole, begins, ends;
+  int slot;                      // partial slot
+  int parts;                     // workgroups that hold a part (0: whole)
+};
+__device__ __forceinline__ Target target_of(const Place& at, int k1, int cost, int wg) {
+  Target t;
+  t.begins = at.k == 0;
+  t.ends = k1 == cost;
+  t.whole = t.begins && t.ends;
+  t.slot = 2 * wg + (t.begins ? 1 : 0);
+  t.parts = t.whole ? 0 : (int)((at.pos + cost - 1) / at.share) - wg + 1;
+  return t;
+}
+
+template <bool kPrefix, bool kJoin>
+__device__ __forceinline__ void note_item(const Parts& parts, const Target& t, const Request& q,
+                                          int row0, int rows, int head, int wg) {
+  if (!kJoin && t.begins && !t.ends && threadIdx.x == 0) {
+    Split s;
+    s.token0 = q.token0;
+    s.row0 = row0;
+    s.rows = rows;
+    s.head = head;
+    s.parts = t.parts;
+    parts.split[wg] = s;
+  }
+}
+
+// m and l of a row that goes to the workspace, and where it went
+template <bool kPrefix, bool kJoin>
+__device__ __forceinline__ void note_row(const Parts& parts, const Target& t, int64_t flat,
+                                         int part_row, float m, float l) {
+  float* pm = t.whole ? parts.whole_ml + flat * 2 : parts.ml + (int64_t)part_row * 2;
+  pm[0] = m;
+  pm[1] = l;
+  if (kJoin && t.begins) {
+    parts.where[flat] = make_int2(part_row, t.parts);
+    if (kPrefix) parts.reset[flat] = make_int2(0, -1);
+  }
+}
+
+// ---- few rows: 16-row tiles -----------------------------------------------------
+// One workgroup of 4 waves; a key tile is 128 keys, 32 per wave.  Every wave
+// holds the same 16 query rows and its own m, l, O over its own keys; the four
+// are joined in LDS once per item.  K and V go from memory to registers, no
+// LDS: a wave reads 16 keys' rows of D bytes as whole lines (lane (n, g): D / 4
+// bytes of key n), and for V lane (n, g) reads bytes n D/16 .. of the 8 keys
+// that its P values stand for, transposes them in registers and converts.  The
+// next unit's 8 KB (D = 128) are in flight while one is computed.
+constexpr int kRowsD = 16;
+constexpr int kKeysD = 128;
+
+template <int D>
+struct Unit {
+  uint32_t k[2][D / 16];   // lane (n, g): D/4 bytes at g D/4 of keys n and 16 + n
+  uint32_t v[8][D / 64];   // lane (n, g): D/16 bytes at n D/16 of keys 4g+i, 16+4g+i
+};
+
+template <int D>
+__device__ __forceinline__ void load_unit(Unit<D>& u, const uint8_t* kc, const uint8_t* vc,
+                                          uint32_t stride, int slot) {
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int s = __shfl(slot, 16 * t + n);
+    const uint8_t* p = kc + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride + g * (D / 4);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p + 16 * i);
+      u.k[t][4 * i] = x.x;
+      u.k[t][4 * i + 1] = x.y;
+      u.k[t][4 * i + 2] = x.z;
+      u.k[t][4 * i + 3] = x.w;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int s = __shfl(slot, (e < 4 ? 0 : 12) + 4 * g + e);
+    const uint8_t* p = vc + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride + n * (D / 16);
+    if constexpr (D == 64) {
+      u.v[e][0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (D == 128) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      u.v[e][0] = x.x;
+      u.v[e][1] = x.y;
+    } else {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      u.v[e][0] = x.x;
+      u.v[e][1] = x.y;
+      u.v[e][2] = x.z;
+      u.v[e][3] = x.w;
+    }
+  }
+}
+
+// V operands of one dword column of the unit: v16[b][e] = byte b of key e
+__device__ __forceinline__ void v_operands(const uint32_t w[8], f16x8 out[4]) {
+  uint32_t lo[4], hi[4];
+  transpose4(w[0], w[1], w[2], w[3], lo);
+  transpose4(w[4], w[5], w[6], w[7], hi);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) out[b] = f16_of_codes(lo[b], hi[b]);
+}
+
+template <int D, bool kPrefix, bool kJoin>
+__global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs args) {
+  constexpr int R = kRowsD, KT = kKeysD, OT = D / 16;
+  constexpr int kPitch = D + 4;                    // floats: rows start in other banks
+  constexpr int kNanWords = D >= 128 ? D / 128 : 1;   // of a lane's D / 4 values
+  __shared__ float s_o[4][R][kPitch];
+  __shared__ float s_ml[4][R][2];
+  __shared__ int64_t s_wave[4], s_found[2];
+  const AttentionArgs& a = args.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const int wg = blockIdx.x;
+  Place at = find_share<kPrefix, R, KT>(a, wg, gridDim.x, s_wave, s_found);
+  if (!kJoin && tid == 0) args.parts.split[wg].parts = 0;
+  const uint32_t stride = (uint32_t)a.Hk * D;
+  const Factor fac = factor_of(a);
+  const float c = fac.c;
+
+  while (at.pos < at.end) {
+    const Request q = load_request<kPrefix>(a, at.r);
+    const int mt = row_tiles(a, q, R);
+    if (at.m >= mt) {                              // a request without queries
+      ++at.r;
+      at.m = at.h = at.k = 0;
+      continue;
+    }
+    const Tiles tl = tiles_of<kPrefix, R, KT>(a, q, at.m);
+    const int cost = cost_of(tl);
+    const int64_t left = at.end - at.pos;
+    const int k1 = uniform((int64_t)(cost - at.k) < left ? cost : at.k + (int)left);
+    const int row0 = at.m * R;
+    const int rest = q.n * a.G - row0;
+    const int rows = uniform(rest < R ? rest : R);
+
+    // this lane's row: queries of row n, k slices of group g
+    const int i_n = n < rows ? (row0 + n) / a.G : 0;
+    const int p_n = kPrefix ? q.keys - 1 : q.p0 + i_n;
+    bf16x8 qf[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) qf[i] = bf16x8{};
+    if (n < rows) {
+      const uint16_t* p = a.q + (int64_t)(q.token0 + i_n) * a.ld_q +
+                          (int64_t)(at.h * a.G + row0 + n - i_n * a.G) * D + g * (D / 4);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) qf[i] = load_query(p + 8 * i, fac.flip);
+    }
+    float m = FP8_NEG_INF, l = 0.0f;
+    f32x4 o[OT];
+#pragma unroll
+    for (int j = 0; j < OT; ++j) o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    NanBits<kNanWords> nans = {};
+
+    const int count = tl.count();
+    const int kend = k1 < count ? k1 : count;      // an item of no keys has no tile
+    if (at.k < kend) {
+      const int32_t* table = kPrefix ? a.prefix_table : a.table + (int64_t)at.r * a.ld_table;
+      const uint8_t* kc = a.kc + (int64_t)at.h * D;
+      const uint8_t* vc = a.vc + (int64_t)at.h * D;
+      auto slot_at = [&](int k) {
+        return k < kend ? slot_of(table, tl.key_tile(k) * KT + wave * 32 + (lane & 31), q.keys,
+                                  a.page, a.num_blocks)
+                        : -1;
+      };
+      Unit<D> next;
+      int slot = slot_at(at.k), slot_next = slot_at(at.k + 1);
+      load_unit<D>(next, kc, vc, stride, slot);
+#pragma unroll 1
+      for (int k = at.k; k < kend; ++k) {
+        Unit<D> now = next;
+        const int kb = tl.key_tile(k) * KT + wave * 32;
+        const int mine = slot;
+        slot = slot_next;
+        if (k + 1 < kend) load_unit<D>(next, kc, vc, stride, slot);
+        slot_next = slot_at(k + 2);
+        const uint32_t mapped = (uint32_t)__ballot(mine >= 0);
+        if (mapped == 0u) continue;                // nothing of these 32 keys is there
+        // S^T: keys 16 t + 4 g + i of row n
+        f32x4 s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                bf16_of_codes(now.k[t][2 * i], now.k[t][2 * i + 1]), qf[i], s[t], 0, 0, 0);
+        }
+        const int last = kb + 31;
+        const bool all = mapped == 0xffffffffu && last <= tl.p_lo &&
+                         (a.window == 0 || tl.p_hi - kb < a.window || last < a.sinks);
+        if (!all) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int b = 16 * t + 4 * g + i;
+              const bool v = ((mapped >> b) & 1u) && sees(kb + b, p_n, a.window, a.sinks);
+              s[t][i] = v ? s[t][i] : FP8_NEG_INF;
+            }
+          // values that are not there are zeros
+          uint32_t nan = 0u;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const bool there = (mapped >> ((e < 4 ? 0 : 12) + 4 * g + e)) & 1u;
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w) {
+              now.v[e][w] = there ? now.v[e][w] : 0u;
+              nan |= nan_codes(now.v[e][w]);
+            }
+          }
+          // a NaN that some rows see and others do not: a zero here, and
+          // noted for the rows that see it
+          if (__ballot(nan != 0u) != 0ull) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+              for (int w = 0; w < D / 64; ++w) now.v[e][w] = without_nans(now.v[e][w]);
+#pragma unroll 1
+            for (int b = 0; b < 32; ++b) {
+              const int sb = __shfl(mine, b);
+              if (sb >= 0 && sees(kb + b, p_n, a.window, a.sinks)) {
+                const uint8_t* p = vc + (uint64_t)(uint32_t)sb * stride + g * (D / 4);
+                if constexpr (D >= 128) {
+                  add_nans(nans, p);
+                } else {                           // 16 values of a lane
+#pragma unroll 1
+                  for (int i = 0; i < 16; ++i)
+                    nans.w[0] |= (uint32_t)((p[i] & 0x7fu) == 0x7fu) << i;
+                }
+              }
+            }
+          }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, s[t][i]);
+        top = max_xor32(max_xor16(top)) * c;
+        const float m_new = __builtin_fmaxf(m, top);
+        const float base = base_of(m_new);
+        const float alpha = __builtin_amdgcn_exp2f(m - base);
+        m = m_new;
+        float sum = 0.0f;
+        f16x8 p;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], c, -base));
+            sum += e;
+            p[4 * t + i] = (_Float16)e;
+          }
+        l = __builtin_fmaf(l, alpha, sum);
+#pragma unroll
+        for (int j = 0; j < OT; ++j) o[j] *= alpha;
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) {
+          uint32_t col[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) col[i] = now.v[i][w];
+          f16x8 vo[4];
+          v_operands(col, vo);
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            o[4 * w + b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vo[b], p, o[4 * w + b], 0, 0, 0);
+        }
+      }
+    }
+    l = sum_xor32(sum_xor16(l));
+
+    // join the four waves: lane (n, g) holds d = (4 g + i) OT + j of row n
+    __syncthreads();                               // the last item's readers are done
+    if (n < rows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < OT; j += 4) {
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int bit = i * OT + j + e;        // of this lane's D / 4 values
+            x[e] = (nans.w[bit / 32] >> (bit % 32)) & 1u ? __builtin_nanf("") : o[j + e][i];
+          }
+          *reinterpret_cast<float4*>(&s_o[wave][n][(4 * g + i) * OT + j]) =
+              make_float4(x[0], x[1], x[2], x[3]);
+        }
+      if (g == 0) {
+        s_ml[wave][n][0] = m;
+        s_ml[wave][n][1] = l;
+      }
+    }
+    __syncthreads();
+    const KernelArgs* fr = fresh_args();
+    const Parts parts = fr->parts;
+    const Target to = target_of(at, k1, cost, wg);
+    // a thread takes 4 values of a row at a time
+    constexpr int kVec = D / 4;
+    for (int x = tid; x < rows * kVec; x += kThreads) {
+      const int row = x / kVec, d = (x - row * kVec) * 4;
+      float mm = s_ml[0][row][0];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) mm = __builtin_fmaxf(mm, s_ml[w][row][0]);
+      const float base = base_of(mm);
+      float ll = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = __builtin_amdgcn_exp2f(s_ml[w][row][0] - base);
+        ll = __builtin_fmaf(s_ml[w][row][1], f, ll);
+        const float4 y = *reinterpret_cast<const float4*>(&s_o[w][row][d]);
+        acc[0] = __builtin_fmaf(y.x, f, acc[0]);
+        acc[1] = __builtin_fmaf(y.y, f, acc[1]);
+        acc[2] = __builtin_fmaf(y.z, f, acc[2]);
+        acc[3] = __builtin_fmaf(y.w, f, acc[3]);
+      }
+      const int rr = row0 + row, i = rr / a.G;
+      const int64_t token = q.token0 + i;
+      const int head = at.h * a.G + rr - i * a.G;
+      const int64_t flat = token * a.Hq + head;
+      if (to.whole && !kJoin) {
+        const float inv = ll == 0.0f ? 0.0f : fr->a.v_scale[0] / ll;
+        const uint32_t w0 = bf16_rne(acc[0] * inv) | (bf16_rne(acc[1] * inv) << 16);
+        const uint32_t w1 = bf16_rne(acc[2] * inv) | (bf16_rne(acc[3] * inv) << 16);
+        *reinterpret_cast<uint2*>(fr->a.out + token * fr->a.ld_out + (int64_t)head * D + d) =
+            make_uint2(w0, w1);
+        if (fr->a.lse && d == 0) fr->a.lse[flat] = (base + __builtin_log2f(ll)) * kLn2;
+      } else {
+        const int part_row = to.slot * R + row;
+        float* po = to.whole ? parts.whole_o + flat * D : parts.o + (int64_t)part_row * D;
+        *reinterpret_cast<float4*>(po + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (d == 0) note_row<kPrefix, kJoin>(parts, to, flat, part_row, mm, ll);
+      }
+    }
+    note_item<kPrefix, kJoin>(parts, to, q, row0, rows, at.h, wg);
+    at.pos += k1 - at.k;
+    at.k = 0;
+    if (++at.h == a.Hk) {
+      at.h = 0;
+      ++at.m;
+    }
+  }
+}
+
+// ---- many rows: 128-row tiles ----------------------------------------------------
+// One workgroup of 4 waves, 32 rows each; a key tile is 64 keys, staged in LDS
+// once for all waves: K as bf16 [key][D], V as fp16 [d][key], both converted
+// on the way in (two waves take K, two take V, which transpose in registers).
+// While a tile is multiplied the next one's codes are on their way to
+// registers; they are converted into the other LDS buffer behind the products,
+// so a tile costs one barrier.  32 x 32 x 16 products: lane (n, g) with
+// n = lane % 32 holds row n of S^T and O^T.
+//
+// LDS rows are cut into 16-byte pieces whose index is XORed with the row's, so
+// that the 32 rows that one read names lie in different banks.  O^T's rows
+// are not d in order: row 32 b + 8 i + 4 g + e is d = g D/2 + 16 b + 4 i + e, which
+// leaves each lane with D / 2 values in a row to store.
+constexpr int kRowsT = 128;
+constexpr int kKeysT = 64;
+
+template <int D, bool kPrefix, bool kJoin>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_kernel(
+    KernelArgs args) {
+  constexpr int R = kRowsT, KT = kKeysT;
+  constexpr int KS = D / 16;                       // k steps of K Q^T
+  constexpr int OB = D / 32;                       // 32-row blocks of O^T
+  constexpr int RAW = D / 8;                       // dwords of codes a thread stages
+  constexpr int kBuf = KT * D * 2;                 // bytes of a K or V buffer
+  constexpr int kPieces = D / 8 < 16 ? D / 8 - 1 : 15;   // K's XOR range
+  __shared__ __attribute__((aligned(16))) uint8_t s_kv[4 * kBuf];   // K0 K1 V0 V1
+  __shared__ __attribute__((aligned(16))) int s_slot[3][KT];   // of tiles k, k + 1 and k + 2
+  __shared__ int s_nan[2];                         // the last tile staged there with a NaN value
+  __shared__ int64_t s_wave[4], s_found[2];
+  const AttentionArgs& a = args.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int n = lane & 31, g = lane >> 5;
+  // neighbouring shares, which read the same keys, on one XCD (workgroups go
+  // round robin over the 8)
+  const int wgs = gridDim.x;
+  const int wg = wgs % 8 == 0 ? (int)(blockIdx.x % 8) * (wgs / 8) + (int)(blockIdx.x / 8)
+                              : (int)blockIdx.x;
+  Place at = find_share<kPrefix, R, KT>(a, wg, wgs, s_wave, s_found);
+  if (!kJoin && tid == 0) args.parts.split[wg].parts = 0;
+  if (tid < 2) s_nan[tid] = -1;
+  const uint32_t stride = (uint32_t)a.Hk * D;
+  const Factor fac = factor_of(a);
+  const float c = fac.c;
+  int serial = 0;                                  // tiles staged so far
+
+  while (at.pos < at.end) {
+    const Request q = load_request<kPrefix>(a, at.r);
+    const int mt = row_tiles(a, q, R);
+    if (at.m >= mt) {
+      ++at.r;
+      at.m = at.h = at.k = 0;
+      continue;
+    }
+    const Tiles tl = tiles_of<kPrefix, R, KT>(a, q, at.m);
+    const int cost = cost_of(tl);
+    const int64_t left = at.end - at.pos;
+    const int k1 = uniform((int64_t)(cost - at.k) < left ? cost : at.k + (int)left);
+    const int row0 = at.m * R;
+    const int rest = q.n * a.G - row0;
+    const int rows = uniform(rest < R ? rest : R);
+
+    const int row = wave * 32 + n;                 // this lane's row of the tile
+    const bool mine = row < rows;
+    const int i_n = mine ? (row0 + row) / a.G : 0;
+    const int p_n = kPrefix ? q.keys - 1 : q.p0 + i_n;
+    bf16x8 qf[KS];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) qf[i] = bf16x8{};
+    if (mine) {
+      const uint16_t* p = a.q + (int64_t)(q.token0 + i_n) * a.ld_q +
+                          (int64_t)(at.h * a.G + row0 + row - i_n * a.G) * D + g * 8;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) qf[i] = load_query(p + 16 * i, fac.flip);
+    }
+    float m = FP8_NEG_INF, l = 0.0f;
+    f32x16 o[OB];
+#pragma unroll
+    for (int b = 0; b < OB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
+    NanBits<D / 64> nans = {};                     // of this lane's D / 2 values
+
+    const int count = tl.count();
+    const int kend = k1 < count ? k1 : count;
+    if (at.k < kend) {
+      const int32_t* table = kPrefix ? a.prefix_table : a.table + (int64_t)at.r * a.ld_table;
+      const uint8_t* kc = a.kc + (int64_t)at.h * D;
+      const uint8_t* vc = a.vc + (int64_t)at.h * D;
+      uint32_t raw[RAW];
+      auto find_slots = [&](int k) {               // wave 0, one key a lane
+        return k < kend ? slot_of(table, tl.key_tile(k) * KT + lane, q.keys, a.page, a.num_blocks)
+                        : -1;
+      };
+      auto fetch = [&](int sb) {                   // codes of a tile to registers
+        if (tid < 128) {
+          const int s = s_slot[sb][tid >> 1];
+          const uint8_t* p =
+              kc + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride + (tid & 1) * (D / 2);
+#pragma unroll
+          for (int i = 0; i < RAW / 4; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4*>(p + 16 * i);
+            raw[4 * i] = x.x;
+            raw[4 * i + 1] = x.y;
+            raw[4 * i + 2] = x.z;
+            raw[4 * i + 3] = x.w;
+          }
+        } else {
+          const int u = tid - 128, ch = u >> 4, x16 = u & 15;
+          const int k0 = (ch >> 1) * 16 + (ch & 1) * 4;
+          const int4 lo = *reinterpret_cast<const int4*>(&s_slot[sb][k0]);
+          const int4 hi = *reinterpret_cast<const int4*>(&s_slot[sb][k0 + 8]);
+          const int s8[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint8_t* p =
+                vc + (uint64_t)(uint32_t)(s8[e] < 0 ? 0 : s8[e]) * stride + x16 * (D / 16);
+            if constexpr (D == 64) {
+              raw[e] = *reinterpret_cast<const uint32_t*>(p);
+            } else if constexpr (D == 128) {
+              const uint2 x = *reinterpret_cast<const uint2*>(p);
+              raw[2 * e] = x.x;
+              raw[2 * e + 1] = x.y;
+            } else {
+              const uint4 x = *reinterpret_cast<const uint4*>(p);
+              raw[4 * e] = x.x;
+              raw[4 * e + 1] = x.y;
+              raw[4 * e + 2] = x.z;
+              raw[4 * e + 3] = x.w;
+            }
+          }
+        }
+      };
+      auto stage = [&](int buf, int sb, int id) {     // converted into LDS
+        if (tid < 128) {
+          const int key = tid >> 1, p0 = (tid & 1) * (D / 16);
+          uint8_t* dst = s_kv + buf * kBuf + key * (2 * D);
+#pragma unroll
+          for (int i = 0; i < RAW / 2; ++i)
+            *reinterpret_cast<bf16x8*>(dst + (((p0 + i) ^ (key & kPieces)) * 16)) =
+                bf16_of_codes(raw[2 * i], raw[2 * i + 1]);
+        } else {
+          const int u = tid - 128, ch = u >> 4, x16 = u & 15;
+          const int k0 = (ch >> 1) * 16 + (ch & 1) * 4;
+          uint8_t* dst = s_kv + (2 + buf) * kBuf;
+          uint32_t nan = 0u;
+          // keys that are not there: zeros, whatever their address held
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const bool there = s_slot[sb][k0 + (e < 4 ? e : e + 4)] >= 0;
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w) {
+              raw[e * (D / 64) + w] = there ? raw[e * (D / 64) + w] : 0u;
+              nan |= nan_codes(raw[e * (D / 64) + w]);
+            }
+          }
+          if (nan != 0u) {                         // zeros here; the tile's rows look again
+            s_nan[buf] = id;
+#pragma unroll
+            for (int i = 0; i < RAW; ++i) raw[i] = without_nans(raw[i]);
+          }
+#pragma unroll
+          for (int w = 0; w < D / 64; ++w) {
+            uint32_t col[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) col[e] = raw[e * (D / 64) + w];
+            f16x8 vo[4];
+            v_operands(col, vo);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const int d = x16 * (D / 16) + 4 * w + b;
+              const int half = d / (D / 2), rem = d % (D / 2);
+              const int vr = (rem / 16) * 32 + ((rem / 4) % 4) * 8 + half * 4 + rem % 4;
+              *reinterpret_cast<f16x8*>(dst + vr * 128 + ((ch ^ vr ^ (vr >> 3)) & 7) * 16) = vo[b];
+            }
+          }
+        }
+      };
+
+      // slots of tiles k and k + 1, the codes of tile k in LDS
+      if (wave == 0) {
+        s_slot[0][lane] = find_slots(at.k);
+        s_slot[1][lane] = find_slots(at.k + 1);
+      }
+      __syncthreads();
+      int cur = 0, s0 = 0, s1 = 1, s2 = 2;
+      fetch(0);
+      stage(0, 0, serial);
+      __syncthreads();
+#pragma unroll 1
+      for (int k = at.k; k < kend; ++k) {
+        const int kb = tl.key_tile(k) * KT;
+        const uint64_t mapped = __ballot(s_slot[s0][lane] >= 0);
+        const bool more = k + 1 < kend;
+        if (more) fetch(s1);
+        int next_slot = -1;
+        if (wave == 0) next_slot = find_slots(k + 2);
+
+        // S^T: block t holds keys 32 t + 8 (v / 4) + 4 g + v % 4 of row n
+        f32x16 s[2];
+        {
+          int piece = (g ^ (n & kPieces)) * 16;    // of k step 0; step i XORs 32 i
+          asm volatile("" : "+v"(piece));          // computed per read, not kept
+          const uint8_t* kr = s_kv + cur * kBuf + n * (2 * D);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int v = 0; v < 16; ++v) s[t][v] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+              s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  *reinterpret_cast<const bf16x8*>(kr + t * (64 * D) + (piece ^ (32 * i))), qf[i],
+                  s[t], 0, 0, 0);
+          }
+        }
+        const int last = kb + KT - 1;
+        const bool all = mapped == ~0ull && last <= tl.p_lo &&
+                         (a.window == 0 || tl.p_hi - kb < a.window || last < a.sinks);
+        if (!all) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+              const int b = 32 * t + 8 * (v / 4) + 4 * g + v % 4;
+              const bool is = ((mapped >> b) & 1u) && sees(kb + b, p_n, a.window, a.sinks);
+              s[t][v] = is ? s[t][v] : FP8_NEG_INF;
+            }
+        }
+        if (s_nan[cur] == serial) {                // NaN values: which ones does this row see?
+#pragma unroll 1
+          for (int b = 0; b < KT; ++b) {
+            const int sb = s_slot[s0][b];
+            if (sb >= 0 && sees(kb + b, p_n, a.window, a.sinks))
+              add_nans(nans, vc + (uint64_t)(uint32_t)sb * stride + g * (D / 2));
+          }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) top = __builtin_fmaxf(top, s[t][v]);
+        top = max_xor32(top) * c;
+        const float m_new = __builtin_fmaxf(m, top);
+        const float base = base_of(m_new);
+        if (__ballot(m_new != m) != 0ull) {        // some row's maximum grew
+          const float alpha = __builtin_amdgcn_exp2f(m - base);
+          l *= alpha;
+#pragma unroll
+          for (int b = 0; b < OB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[b][i] *= alpha;
+          m = m_new;
+        }
+        float sum = 0.0f;
+        f16x8 p[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][v], c, -base));
+            sum += e;
+            p[2 * t + v / 8][v % 8] = (_Float16)e;
+          }
+        l += sum;
+        {
+          int piece = ((g ^ n ^ (n >> 3)) & 7) * 16;   // of row n, k step 0
+          asm volatile("" : "+v"(piece));
+          const uint8_t* vr = s_kv + (2 + cur) * kBuf + n * 128;
+#pragma unroll
+          for (int b = 0; b < OB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                  *reinterpret_cast<const f16x8*>(vr + b * 4096 +
+                                                  (piece ^ (32 * i) ^ ((b & 1) * 64))),
+                  p[i], o[b], 0, 0, 0);
+        }
+        ++serial;
+        if (more) stage(cur ^ 1, s1, serial);
+        if (wave == 0) s_slot[s2][lane] = next_slot;   // tile k - 1's place
+        __syncthreads();
+        cur ^= 1;
+        const int done = s0;
+        s0 = s1;
+        s1 = s2;
+        s2 = done;
+      }
+    }
+    l = sum_xor32(l);
+
+    const KernelArgs* fr = fresh_args();
+    const Parts parts = fr->parts;
+    const Target to = target_of(at, k1, cost, wg);
+    if (mine) {
+      const int64_t token = q.token0 + i_n;
+      const int head = at.h * a.G + row0 + row - i_n * a.G;
+      const int64_t flat = token * a.Hq + head;
+      bool any = false;
+#pragma unroll
+      for (int w = 0; w < D / 64; ++w) any |= nans.w[w] != 0u;
+      if (any) {
+#pragma unroll
+        for (int b = 0; b < OB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int bit = 16 * b + i;
+            o[b][i] = (nans.w[bit / 32] >> (bit % 32)) & 1u ? __builtin_nanf("") : o[b][i];
+          }
+      }
+      if (to.whole && !kJoin) {
+        const float inv = l == 0.0f ? 0.0f : fr->a.v_scale[0] / l;
+        uint16_t* po = fr->a.out + token * fr->a.ld_out + (int64_t)head * D + g * (D / 2);
+#pragma unroll
+        for (int b = 0; b < OB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; i += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = bf16_rne(o[b][i + 2 * e] * inv) | (bf16_rne(o[b][i + 2 * e + 1] * inv) << 16);
+            *reinterpret_cast<uint4*>(po + 16 * b + i) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        if (fr->a.lse && g == 0) fr->a.lse[flat] = (base_of(m) + __builtin_log2f(l)) * kLn2;
+      } else {
+        const int part_row = to.slot * R + row;
+        float* po = (to.whole ? parts.whole_o + flat * D : parts.o + (int64_t)part_row * D) +
+                    g * (D / 2);
+#pragma unroll
+        for (int b = 0; b < OB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(po + 16 * b + i) =
+                make_float4(o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]);
+        if (g == 0) note_row<kPrefix, kJoin>(parts, to, flat, part_row, m, l);
+      }
+    }
+    note_item<kPrefix, kJoin>(parts, to, q, row0, rows, at.h, wg);
+    at.pos += k1 - at.k;
+    at.k = 0;
+    if (++at.h == a.Hk) {
+      at.h = 0;
+      ++at.m;
+    }
+  }
+}
+
+// ---- joining the parts ------------------------------------------------------------
+// Part j of a result whose first part is row f of ml / o: the first workgroup
+// left it in its odd slot, the ones behind it in their even slots.
+__device__ __forceinline__ int64_t part_row(int64_t f, int j, int R) {
+  return j == 0 ? f : f + (int64_t)(2 * j - 1) * R;
+}
+
+__device__ __forceinline__ float wave_fmax(float x) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) x = __builtin_fmaxf(x, __shfl_xor(x, d));
+  return x;
+}
+
+// maximum of the parts' m over a wave
+__device__ __forceinline__ float parts_max(const float* ml, int64_t f, int np, int R) {
+  float m = FP8_NEG_INF;
+  for (int j = threadIdx.x & 63; j < np; j += 64)
+    m = __builtin_fmaxf(m, ml[part_row(f, j, R) * 2]);
+  return wave_fmax(m);
+}
+
+template <int D>
+struct Sum {
+  float l, o[D / 64];          // lane i: values i D/64 ..
+};
+
+template <int D>
+__device__ __forceinline__ void add_row(Sum<D>& s, const float* ml, const float* o, int64_t row,
+                                        float base) {
+  const int lane = threadIdx.x & 63;
+  const float f = __builtin_amdgcn_exp2f(ml[row * 2] - base);
+  s.l = __builtin_fmaf(ml[row * 2 + 1], f, s.l);
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i)
+    s.o[i] = __builtin_fmaf(o[row * D + lane * (D / 64) + i], f, s.o[i]);
+}
+
+template <int D>
+__device__ __forceinline__ void add_parts(Sum<D>& s, const float* ml, const float* o, int64_t f,
+                                          int np, int R, float base, int j0, int step) {
+  int j = j0;
+  for (; j + 3 * step < np; j += 4 * step) {       // four parts' loads together
+#pragma unroll
+    for (int u = 0; u < 4; ++u) add_row<D>(s, ml, o, part_row(f, j + u * step, R), base);
+  }
+  for (; j < np; j += step) add_row<D>(s, ml, o, part_row(f, j, R), base);
+}
+
+template <int D>
+__device__ __forceinline__ void write_row(const AttentionArgs& a, const Sum<D>& s, float base,
+                                          int64_t token, int head) {
+  const int lane = threadIdx.x & 63;
+  const float inv = s.l == 0.0f ? 0.0f : a.v_scale[0] / s.l;
+  uint16_t* p = a.out + token * a.ld_out + (int64_t)head * D + lane * (D / 64);
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) p[i] = (uint16_t)bf16_rne(s.o[i] * inv);
+  if (a.lse && lane == 0) a.lse[token * a.Hq + head] = (base + __builtin_log2f(s.l)) * kLn2;
+}
+
+// Items that shares cut: block (w, y) joins rows y, y + gridDim.y, .. of the
+// item that starts in workgroup w's share.  With many parts the four waves
+// share a row's parts, else each takes rows of its own.
+template <int D>
+__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs a, Parts parts,
+                                                                  int R) {
+  __shared__ float s_l[4], s_o[4][D];
+  const Split sp = parts.split[blockIdx.x];
+  if (sp.parts == 0) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool wide = sp.parts > 8;
+  const int first = wide ? blockIdx.y : blockIdx.y * 4 + wave;
+  const int step = wide ? gridDim.y : gridDim.y * 4;
+  for (int row = first; row < sp.rows; row += step) {
+    const int64_t f = ((int64_t)2 * blockIdx.x + 1) * R + row;
+    const float base = base_of(parts_max(parts.ml, f, sp.parts, R));
+    Sum<D> s = {};
+    add_parts<D>(s, parts.ml, parts.o, f, sp.parts, R, base, wide ? wave : 0, wide ? 4 : 1);
+    if (wide) {
+      __syncthreads();
+      if (lane == 0) s_l[wave] = s.l;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) s_o[wave][lane * (D / 64) + i] = s.o[i];
+      __syncthreads();
+      if (wave != 0) continue;
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        s.l += s_l[w];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) s.o[i] += s_o[w][lane * (D / 64) + i];
+      }
+    }
+    const int rho = sp.row0 + row, i = rho / a.G;
+    write_row<D>(a, s, base, sp.token0 + i, sp.head * a.G + rho - i * a.G);
+  }
+}
+
+// Shared prefix: a wave joins a row's parts of the prefix and of its request.
+template <int D>
+__global__ __launch_bounds__(kThreads) void attention_prefix_join_kernel(AttentionArgs a, Parts p1,
+                                                                         int R1, Parts p2,
+                                                                         int R2) {
+  const int64_t flat = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (flat >= (int64_t)a.T * a.Hq) return;
+  const int2 w1 = p1.where[flat], w2 = p2.where[flat];
+  if (w2.y < 0) return;                            // a row of no request
+  const float m1 = w1.y ? parts_max(p1.ml, w1.x, w1.y, R1) : p1.whole_ml[flat * 2];
+  const float m2 = w2.y ? parts_max(p2.ml, w2.x, w2.y, R2) : p2.whole_ml[flat * 2];
+  const float base = base_of(__builtin_fmaxf(m1, m2));
+  Sum<D> s = {};
+  if (w1.y) add_parts<D>(s, p1.ml, p1.o, w1.x, w1.y, R1, base, 0, 1);
+  else add_row<D>(s, p1.whole_ml, p1.whole_o, flat, base);
+  if (w2.y) add_parts<D>(s, p2.ml, p2.o, w2.x, w2.y, R2, base, 0, 1);
+  else add_row<D>(s, p2.whole_ml, p2.whole_o, flat, base);
+  const int64_t token = flat / a.Hq;
+  write_row<D>(a, s, base, token, (int)(flat - token * a.Hq));
+}
+
+// ---- host ---------------------------------------------------------------------------
+int compute_units() {
+  static std::atomic<int> cached[64];
+  int dev = 0, n = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+        n <= 0)
+      return 256;
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Rows per request, on average, from which 128-row tiles are used.
+bool many_rows(int64_t T, int64_t B, int64_t G) { return T * G > 32 * B; }
+
+struct Shape {
+  bool tiles;                   // 128-row tiles
+  int wgs, R;
+};
+
+Shape shape_of(bool tiles, int D) {
+  const int cus = compute_units();
+  Shape s;
+  s.tiles = tiles;
+  s.R = tiles ? kRowsT : kRowsD;
+  s.wgs = tiles ? (D == 256 ? cus : 2 * cus) : (D == 256 ? 2 * cus : 3 * cus);
+  return s;
+}
+
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Lays a launch's parts out at ws + at (ws may be null) and moves `at` behind.
+Parts lay_out(uint8_t* ws, size_t& at, const Shape& s, int64_t D, int64_t rows_joined) {
+  Parts p = {};
+  auto take = [&](size_t bytes) {
+    uint8_t* x = ws ? ws + at : nullptr;
+    at = align256(at + bytes);
+    return x;
+  };
+  const size_t rows = (size_t)2 * s.wgs * s.R;
+  p.ml = (float*)take(rows * 2 * sizeof(float));
+  p.o = (float*)take(rows * D * sizeof(float));
+  if (rows_joined > 0) {
+    p.where = (int2*)take(rows_joined * sizeof(int2));
+    p.whole_ml = (float*)take(rows_joined * 2 * sizeof(float));
+    p.whole_o = (float*)take(rows_joined * D * sizeof(float));
+  } else {
+    p.split = (Split*)take(s.wgs * sizeof(Split));
+  }
+  return p;
+}
+
+template <int D, bool kPrefix, bool kJoin>
+void launch_main(const AttentionArgs& a, const Parts& p, const Shape& s, hipStream_t st) {
+  const KernelArgs k = {a, p};
+  if (s.tiles)
+    hipLaunchKernelGGL((attention_tile_kernel<D, kPrefix, kJoin>), dim3(s.wgs), dim3(kThreads), 0,
+                       st, k);
+  else
+    hipLaunchKernelGGL((attention_rows_kernel<D, kPrefix, kJoin>), dim3(s.wgs), dim3(kThreads), 0,
+                       st, k);
+}
+
+template <int D>
+hipError_t launch_d(const AttentionArgs& a, hipStream_t st) {
+  size_t at = 0;
+  if (!a.prefix_len) {
+    const Shape s = shape_of(many_rows(a.T, a.B, a.G), D);
+    const Parts p = lay_out(a.ws, at, s, D, 0);
+    launch_main<D, false, false>(a, p, s, st);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(attention_join_kernel<D>, dim3(s.wgs, s.tiles ? 8 : 4), dim3(kThreads), 0,
+                       st, a, p, s.R);
+    return hipGetLastError();
+  }
+  const int64_t rows = (int64_t)a.T * a.Hq;
+  const Shape s1 = shape_of((int64_t)a.T * a.G > kRowsD, D);
+  const Shape s2 = shape_of(many_rows(a.T, a.B, a.G), D);
+  Parts p1 = lay_out(a.ws, at, s1, D, rows), p2 = lay_out(a.ws, at, s2, D, rows);
+  p1.reset = p2.where;
+  launch_main<D, true, true>(a, p1, s1, st);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  launch_main<D, false, true>(a, p2, s2, st);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(attention_prefix_join_kernel<D>, dim3((uint32_t)((rows + 3) / 4)),
+                     dim3(kThreads), 0, st, a, p1, s1.R, p2, s2.R);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attention_workspace(bool prefix, int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
+  const int64_t G = Hq / Hk;
+  size_t at = 0;
+  if (!prefix) {
+    lay_out(nullptr, at, shape_of(many_rows(T, B, G), (int)D), D, 0);
+  } else {
+    lay_out(nullptr, at, shape_of(T * G > kRowsD, (int)D), D, T * Hq);
+    lay_out(nullptr, at, shape_of(many_rows(T, B, G), (int)D), D, T * Hq);
+  }
+  return at;
+}
+
+hipError_t launch_attention(const AttentionArgs& a, int D, hipStream_t st) {
+  switch (D) {
+    case 64: return launch_d<64>(a, st);
+    case 128: return launch_d<128>(a, st);
+    default: return launch_d<256>(a, st);
+  }
+}
+
+}  // namespace fp8k
