@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import _cache, _check, _device_tensor, _i64, _int, _stream, _sz, _tokens, _vp, _workspace
+from ._lib import _check, _device_tensor, _i64, _int, _sz, _vp, _workspace
 
 _f32 = ctypes.c_float
 
@@ -53,25 +53,47 @@ def lib():
     return _bound
 
 
+def _on(t, name, dtype, device):
+    """A device tensor of this type on this device (the checks of
+    _device_tensor, which says what is wrong)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device:
+        _device_tensor(t, name, dtype, device)
+
+
+def _device_of(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.device
+
+
 def _vector(t, name, dtype, device, n=None):
     """A contiguous 1-D device tensor (of n elements) -> its pointer."""
-    _device_tensor(t, name, dtype, device)
+    _on(t, name, dtype, device)
     if t.dim() != 1 or (n is not None and t.shape[0] != n):
         raise ValueError(f"{name} must be 1-D" + (f" of {n} elements" if n is not None else ""))
-    if t.stride(0) != 1 and t.shape[0] > 1:
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _heads(t, name):
-    """_tokens, where an empty step's strides do not matter."""
-    if t.dim() == 3 and t.numel() == 0 and t.dtype == torch.bfloat16 and t.is_cuda:
-        return (*t.shape, t.shape[1] * t.shape[2])
-    return _tokens(t, name)
+def _heads(t, name, device):
+    """[T, H, D] bf16 with each token's H * D values contiguous -> (T, H, D, token stride)."""
+    _on(t, name, torch.bfloat16, device)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, H, D]")
+    T, H, D = t.shape
+    ld, sh, sd = t.stride()
+    if T * H * D == 0:
+        return T, H, D, H * D
+    if sd != 1 or (sh != D and H > 1):
+        raise ValueError(f"{name} must be [T, H, D] with contiguous heads")
+    return T, H, D, (ld if T > 1 else H * D)
 
 
 def _scale(t, name, device):
-    _device_tensor(t, name, torch.float32, device)
+    _on(t, name, torch.float32, device)
     if t.numel() != 1:
         raise ValueError(f"{name} must hold one value")
     return t.data_ptr()
@@ -79,21 +101,37 @@ def _scale(t, name, device):
 
 def _block_table(t, name, device, rows):
     """[rows, width] int32 with unit column stride -> (pointer, row stride, width)."""
-    _device_tensor(t, name, torch.int32, device)
+    _on(t, name, torch.int32, device)
     if t.dim() != 2 or t.shape[0] != rows:
         raise ValueError(f"{name} must be [{rows}, width]")
-    if t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1:
+    width, (ld, step) = t.shape[1], t.stride()
+    if step != 1 and width > 1 and rows > 0:
         raise ValueError(f"{name} must have unit column stride")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else t.shape[1]), t.shape[1]
+    return t.data_ptr(), (ld if rows > 1 else width), width
 
 
 def _caches(key_cache, value_cache, device):
-    shape = _cache(key_cache, "key_cache")
-    if _cache(value_cache, "value_cache") != shape:
+    """Both paged caches -> (blocks, block_size, H, D)."""
+    for c, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
+        _on(c, name, torch.uint8, device)
+        if c.dim() != 4 or not c.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [blocks, block_size, H, D] tensor")
+    if value_cache.shape != key_cache.shape:
         raise ValueError("key_cache and value_cache shapes differ")
-    if key_cache.device != device or value_cache.device != device:
-        raise ValueError(f"the caches must be tensors on {device}")
-    return shape
+    return key_cache.shape
+
+
+def _raw_stream(device):
+    """Handle of the device's current stream (no Stream object around it)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _call(device, call):
+    """Runs call() with `device` current."""
+    if torch.cuda.current_device() == device.index:
+        return call()
+    with torch.cuda.device(device):
+        return call()
 
 
 def kv_slot_map(computed_lens, new_lens, block_table, free_blocks, block_size, num_tokens,
@@ -108,32 +146,30 @@ def kv_slot_map(computed_lens, new_lens, block_table, free_blocks, block_size, n
     [B], blocks_taken int32 [1]); slots and positions behind the last token
     are -1, and so are slots of tokens that no free block was left for
     (blocks_taken then exceeds the number of free blocks)."""
-    dev = computed_lens.device
-    _vector(computed_lens, "computed_lens", torch.int32, dev)
+    dev = _device_of(computed_lens, "computed_lens")
+    computed = _vector(computed_lens, "computed_lens", torch.int32, dev)
     B, T = computed_lens.shape[0], int(num_tokens)
     if T < 0:
         raise ValueError("num_tokens must not be negative")
-    with torch.cuda.device(dev):
-        if slot_mapping is None:
-            slot_mapping = torch.empty(T, dtype=torch.int64, device=dev)
-        if positions is None:
-            positions = torch.empty(T, dtype=torch.int64, device=dev)
-        if query_offsets is None:
-            query_offsets = torch.empty(B + 1, dtype=torch.int32, device=dev)
-        if seq_lens is None:
-            seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        if blocks_taken is None:
-            blocks_taken = torch.empty(1, dtype=torch.int32, device=dev)
-        table, ld, width = _block_table(block_table, "block_table", dev, B)
-        free = _vector(free_blocks, "free_blocks", torch.int32, dev)
-        _check(lib().fp8_kv_slot_map(
-            computed_lens.data_ptr(), _vector(new_lens, "new_lens", torch.int32, dev, B), B,
-            int(block_size), table, ld, width, free, free_blocks.shape[0],
-            _vector(slot_mapping, "slot_mapping", torch.int64, dev, T),
+    if slot_mapping is None:
+        slot_mapping = torch.empty(T, dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty(T, dtype=torch.int64, device=dev)
+    if query_offsets is None:
+        query_offsets = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    if seq_lens is None:
+        seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    if blocks_taken is None:
+        blocks_taken = torch.empty(1, dtype=torch.int32, device=dev)
+    table, ld, width = _block_table(block_table, "block_table", dev, B)
+    args = (computed, _vector(new_lens, "new_lens", torch.int32, dev, B), B, int(block_size),
+            table, ld, width, _vector(free_blocks, "free_blocks", torch.int32, dev),
+            free_blocks.shape[0], _vector(slot_mapping, "slot_mapping", torch.int64, dev, T),
             _vector(positions, "positions", torch.int64, dev, T), T,
             _vector(query_offsets, "query_offsets", torch.int32, dev, B + 1),
             _vector(seq_lens, "seq_lens", torch.int32, dev, B),
-            _vector(blocks_taken, "blocks_taken", torch.int32, dev, 1), _stream(computed_lens)))
+            _vector(blocks_taken, "blocks_taken", torch.int32, dev, 1))
+    _check(_call(dev, lambda: lib().fp8_kv_slot_map(*args, _raw_stream(dev))))
     return slot_mapping, positions, query_offsets, seq_lens, blocks_taken
 
 
@@ -148,35 +184,33 @@ def qk_norm_rope_cache(query, key, value, q_weight, k_weight, cos_sin, positions
     rot_dim < D rotates the first rot_dim values.  interleaved pairs
     neighbours instead of halves.  Tokens whose position is outside the table
     are padding: their rows of query_out stay as they were."""
-    T, Hq, D, ld_q = _heads(query, "query")
-    Tk, Hk, Dk, ld_k = _heads(key, "key")
-    Tv, Hv, Dv, ld_v = _heads(value, "value")
-    if (Tk, Dk) != (T, D) or (Tv, Hv, Dv) != (T, Hk, D):
+    dev = _device_of(query, "query")
+    T, Hq, D, ld_q = _heads(query, "query", dev)
+    Tk, Hk, Dk, ld_k = _heads(key, "key", dev)
+    Tv, Hv, Dv, ld_v = _heads(value, "value", dev)
+    if Tk != T or Dk != D or Tv != T or Hv != Hk or Dv != D:
         raise ValueError("query, key and value shapes do not match")
-    dev = query.device
-    if key.device != dev or value.device != dev:
-        raise ValueError(f"key and value must be tensors on {dev}")
     nb, bs, Hc, Dc = _caches(key_cache, value_cache, dev)
-    if (Hc, Dc) != (Hk, D):
+    if Hc != Hk or Dc != D:
         raise ValueError("cache shapes do not match the tokens")
-    _device_tensor(cos_sin, "cos_sin", torch.float32, dev)
+    _on(cos_sin, "cos_sin", torch.float32, dev)
     if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be a contiguous [positions, rot_dim] tensor")
-    with torch.cuda.device(dev):
-        if query_out is None:
-            query_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-        To, Ho, Do, ld_o = _heads(query_out, "query_out")
-        if (To, Ho, Do) != (T, Hq, D) or query_out.device != dev:
-            raise ValueError(f"query_out must be [{T}, {Hq}, {D}] on {dev}")
-        _check(lib().fp8_qk_norm_rope_cache(
-            query.data_ptr(), ld_q, key.data_ptr(), ld_k, value.data_ptr(), ld_v,
+    if query_out is None:
+        query_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    To, Ho, Do, ld_o = _heads(query_out, "query_out", dev)
+    if To != T or Ho != Hq or Do != D:
+        raise ValueError(f"query_out must be [{T}, {Hq}, {D}]")
+    max_pos, rot = cos_sin.shape
+    args = (query.data_ptr(), ld_q, key.data_ptr(), ld_k, value.data_ptr(), ld_v,
             _vector(q_weight, "q_weight", torch.bfloat16, dev, D),
             _vector(k_weight, "k_weight", torch.bfloat16, dev, D), float(eps), cos_sin.data_ptr(),
-            cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
+            max_pos, rot, int(bool(interleaved)),
             _vector(positions, "positions", torch.int64, dev, T),
             _vector(slot_mapping, "slot_mapping", torch.int64, dev, T), T, Hq, Hk, D,
             query_out.data_ptr(), ld_o, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs,
-            _scale(k_scale, "k_scale", dev), _scale(v_scale, "v_scale", dev), _stream(query)))
+            _scale(k_scale, "k_scale", dev), _scale(v_scale, "v_scale", dev))
+    _check(_call(dev, lambda: lib().fp8_qk_norm_rope_cache(*args, _raw_stream(dev))))
     return query_out
 
 
@@ -187,52 +221,49 @@ def attention_workspace_bytes(T, B, Hq, Hk, D, shared_prefix=False):
                                                    int(Hq), int(Hk), int(D)))
 
 
-def _attention(query, key_cache, value_cache, prefix_table, prefix_len, block_table, seq_lens,
-               query_offsets, k_scale, v_scale, scale, window, sinks, out, lse, workspace):
-    T, Hq, D, ld_q = _heads(query, "query")
-    dev = query.device
+def _attention(query, key_cache, value_cache, prefix, block_table, seq_lens, query_offsets, k_scale,
+               v_scale, scale, window, sinks, out, lse, workspace):
+    """Both attention calls; prefix: None or (prefix_table, prefix_len)."""
+    dev = _device_of(query, "query")
+    T, Hq, D, ld_q = _heads(query, "query", dev)
     nb, bs, Hk, Dc = _caches(key_cache, value_cache, dev)
     if Dc != D:
         raise ValueError("query and cache head sizes differ")
     lens = _vector(seq_lens, "seq_lens", torch.int32, dev)
     B = seq_lens.shape[0]
-    offs = _vector(query_offsets, "query_offsets", torch.int32, dev, B + 1)
-    table, ld_t, width = _block_table(block_table, "block_table", dev, B)
-    ks, vs = _scale(k_scale, "k_scale", dev), _scale(v_scale, "v_scale", dev)
-    shared = prefix_table is not None
-    if shared:
-        p_table = _vector(prefix_table, "prefix_table", torch.int32, dev)
-        p_len = _vector(prefix_len, "prefix_len", torch.int32, dev, 1)
-    if scale is None:
-        scale = D ** -0.5
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-        To, Ho, Do, ld_o = _heads(out, "out")
-        if (To, Ho, Do) != (T, Hq, D) or out.device != dev:
-            raise ValueError(f"out must be [{T}, {Hq}, {D}] on {dev}")
-        lse_ptr = None
-        if lse is not None:
-            _device_tensor(lse, "lse", torch.float32, dev, (T, Hq))
-            if not lse.is_contiguous():
-                raise ValueError("lse must be contiguous")
-            lse_ptr = lse.data_ptr()
-        l = lib()
-        if workspace is None:
-            n = int(l.fp8_attention_workspace_bytes(int(shared), T, B, Hq, Hk, D))
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        ws_ptr, ws_len = _workspace(workspace, dev)
-        if shared:
-            _check(l.fp8_prefix_attention(
-                query.data_ptr(), ld_q, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs,
-                p_table, prefix_table.shape[0], p_len, table, ld_t, width, lens, offs, B, ks, vs,
-                float(scale), out.data_ptr(), ld_o, lse_ptr, T, Hq, Hk, D, ws_ptr, ws_len,
-                _stream(query)))
-        else:
-            _check(l.fp8_paged_attention(
-                query.data_ptr(), ld_q, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs,
-                table, ld_t, width, lens, offs, B, ks, vs, float(scale), int(window), int(sinks),
-                out.data_ptr(), ld_o, lse_ptr, T, Hq, Hk, D, ws_ptr, ws_len, _stream(query)))
+    table = _block_table(block_table, "block_table", dev, B)
+    batch = (*table, lens, _vector(query_offsets, "query_offsets", torch.int32, dev, B + 1), B,
+             _scale(k_scale, "k_scale", dev), _scale(v_scale, "v_scale", dev),
+             float(D ** -0.5 if scale is None else scale))
+    if prefix is not None:
+        batch = (_vector(prefix[0], "prefix_table", torch.int32, dev), prefix[0].shape[0],
+                 _vector(prefix[1], "prefix_len", torch.int32, dev, 1), *batch)
+    else:
+        batch = (*batch, int(window), int(sinks))
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    To, Ho, Do, ld_o = _heads(out, "out", dev)
+    if To != T or Ho != Hq or Do != D:
+        raise ValueError(f"out must be [{T}, {Hq}, {D}]")
+    lse_ptr = None
+    if lse is not None:
+        _on(lse, "lse", torch.float32, dev)
+        if lse.shape != (T, Hq) or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous [{T}, {Hq}] tensor")
+        lse_ptr = lse.data_ptr()
+
+    def call():
+        l, ws = lib(), workspace
+        if ws is None:
+            n = l.fp8_attention_workspace_bytes(int(prefix is not None), T, B, Hq, Hk, D)
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        ws_ptr, ws_len = _workspace(ws, dev)
+        f = l.fp8_paged_attention if prefix is None else l.fp8_prefix_attention
+        return f(query.data_ptr(), ld_q, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs,
+                 *batch, out.data_ptr(), ld_o, lse_ptr, T, Hq, Hk, D, ws_ptr, ws_len,
+                 _raw_stream(dev))
+
+    _check(_call(dev, call))
     return out
 
 
@@ -247,8 +278,8 @@ def paged_attention(query, key_cache, value_cache, block_table, seq_lens, query_
     `window` keys and the first `sinks`.  scale defaults to D ** -0.5; lse
     (float32 [T, Hq]) gets the log-sum-exp of the scores.  Rows that see no key
     are zeros (lse -inf), rows of no request stay as they were."""
-    return _attention(query, key_cache, value_cache, None, None, block_table, seq_lens,
-                      query_offsets, k_scale, v_scale, scale, window, sinks, out, lse, workspace)
+    return _attention(query, key_cache, value_cache, None, block_table, seq_lens, query_offsets,
+                      k_scale, v_scale, scale, window, sinks, out, lse, workspace)
 
 
 def prefix_attention(query, key_cache, value_cache, prefix_table, prefix_len, block_table,
@@ -260,5 +291,5 @@ def prefix_attention(query, key_cache, value_cache, prefix_table, prefix_len, bl
     prefix's keys and values are read once for the whole batch."""
     if prefix_table is None or prefix_len is None:
         raise TypeError("prefix_table and prefix_len must be tensors")
-    return _attention(query, key_cache, value_cache, prefix_table, prefix_len, block_table,
+    return _attention(query, key_cache, value_cache, (prefix_table, prefix_len), block_table,
                       seq_lens, query_offsets, k_scale, v_scale, scale, 0, 0, out, lse, workspace)

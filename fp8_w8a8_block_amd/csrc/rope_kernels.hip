@@ -10,8 +10,11 @@
 // each, one 16-byte load; the mean is a butterfly over the L lanes, and the
 // rotation's partner (D / 2 away) sits in another lane of the same head, or in
 // the lane itself when pairs are neighbours.  The kernel streams: a lane group
-// takes `per` heads of one token, all loads of up to 4 heads issued together,
-// and reads the token's angles once for them.
+// takes several heads of one token, reads the token's angles once for them and
+// has the next head's load in flight while it works on one.  8191 tokens of 32
+// + 8 + 8 heads of 128 (189 MB) take 42 us, 4.5 TB/s, where a large copy moves
+// 4.85; more loads in flight per lane (2, 4, 8 heads) cost occupancy and time
+// (44, 47, 65 us).
 #include "attention_launch.h"
 #include "device_common.h"
 #include "launch.h"
@@ -20,27 +23,75 @@ namespace fp8k {
 
 namespace {
 
-constexpr int kUnroll = 4;
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ uint32_t bf16_rne(float f) {
-  return f != f ? 0x7fc0u : f32_to_bf16_rne(f);
+// two fp32 to bf16, round to nearest even, in one instruction
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
-// L lanes per head; per heads (of Hq + 2 Hk) per lane group and pass.
+// 1 / sqrt(x), x >= 0, within 1 ulp; the instruction does not take subnormals
+__device__ __forceinline__ float rsqrt_of(float x) {
+  const bool tiny = x < 0x1p-100f;
+  const float r = __builtin_amdgcn_rsqf(tiny ? x * 0x1p+100f : x);
+  return tiny ? r * 0x1p+50f : r;
+}
+
+// E4M3 codes of 8 fp32 values divided by a static scale.  The quotient takes
+// the steps of quant8_static; for an fp32 dividend it may be off by one ulp of
+// fp32 (a bf16 one is exact), 2^-19 of an E4M3 step.
+__device__ __forceinline__ uint2 quant8_f32(const float z[8], const StaticDivisor& d) {
+  bool direct = !d.fast;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) direct |= z[e] != z[e];
+  uint32_t o[2] = {0u, 0u};
+  if (direct) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      o[e / 4] |= (uint32_t)e4m3_encode_one(z[e] / d.s) << (8 * (e & 3));
+    return make_uint2(o[0], o[1]);
+  }
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // s' is below 2, so what is cut here has a quotient beyond 448
+    const float x = __builtin_ldexpf(z[e], d.k);
+    const float xa = __builtin_amdgcn_fmed3f(x, -1024.0f, 1024.0f);
+    const float q0 = xa * d.r;
+    const float r = __builtin_fmaf(-q0, d.sp, xa);
+    q[e] = __builtin_amdgcn_fmed3f(__builtin_fmaf(r, d.r, q0), -kE4M3Max, kE4M3Max);
+  }
+  o[0] = e4m3_pack4_mag(q[0], q[1], q[2], q[3]) ^ d.sign;
+  o[1] = e4m3_pack4_mag(q[4], q[5], q[6], q[7]) ^ d.sign;
+  return make_uint2(o[0], o[1]);
+}
+
+// L lanes per head.  `chunks` lane groups share a token's Hq + 2 Hk heads: group
+// j takes heads j, j + chunks, ..., so that a wave's groups read neighbouring
+// heads and are mostly all at queries, at keys or at values.
 template <int L, bool kInterleaved>
-__global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, int32_t per,
-                                                        int32_t chunks) {
-  const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+__global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, uint32_t chunks) {
+  const uint32_t item = blockIdx.x * (256u / L) + threadIdx.x / L;
   const int c = threadIdx.x % L;                    // this lane's 8 values of the head
-  const int64_t t = item / chunks;
-  if (t >= a.T) return;                             // whole lane groups leave together
-  const int h0 = (int)(item - t * chunks) * per;
+  const uint32_t t32 = item / chunks;
+  if (t32 >= a.T) return;                           // whole lane groups leave together
+  const int64_t t = t32;
   const int heads = a.Hq + 2 * a.Hk;
-  const int h1 = h0 + per < heads ? h0 + per : heads;
+  const int h0 = (int)(item - t32 * chunks);
+  const bool live = c * 8 < a.D;
+
+  auto fetch = [&](int h) {
+    const uint16_t* p = h < a.Hq          ? a.q + t * a.ld_q + (int64_t)h * a.D
+                        : h < a.Hq + a.Hk ? a.k + t * a.ld_k + (int64_t)(h - a.Hq) * a.D
+                                          : a.v + t * a.ld_v + (int64_t)(h - a.Hq - a.Hk) * a.D;
+    return h < heads && live ? *reinterpret_cast<const uint4*>(p + c * 8)
+                             : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 next = fetch(h0);                           // on its way while the angles are found
   const int64_t pos = a.positions[t], slot = a.slots[t];
   if (pos < 0 || pos >= a.max_pos) return;
   const bool keep = slot >= 0 && slot < a.capacity;
-  const bool live = c * 8 < a.D;
   const bool turns = c * 8 < a.rot;
   const int half = a.rot / 2;
 
@@ -78,81 +129,56 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, int32_t 
   }
   // lane of the rotation's other half (itself where nothing turns)
   const int partner = !turns ? c : c * 8 < half ? c + half / 8 : c - half / 8;
-  const int lane_base = (threadIdx.x & 63) - c;
+  const int partner_lane = (threadIdx.x & 63) - c + partner;
 
   uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
   if (live) {
     wq = *reinterpret_cast<const uint4*>(a.qw + c * 8);
     wk = *reinterpret_cast<const uint4*>(a.kw + c * 8);
   }
-  const float k_scale = a.k_scale[0];
+  const StaticDivisor kd = make_static_divisor(a.k_scale[0]);
   const StaticDivisor vd = make_static_divisor(a.v_scale[0]);
   const float inv_d = 1.0f / (float)a.D;
 
-  for (int h = h0; h < h1; h += kUnroll) {
-    uint4 x[kUnroll];
+  for (int h = h0; h < heads; h += (int)chunks) {
+    const uint4 x = next;
+    next = fetch(h + (int)chunks);
+    if (h >= a.Hq + a.Hk) {                         // a value head: stored as it is
+      if (keep && live)
+        *reinterpret_cast<uint2*>(a.vc + (slot * a.Hk + (h - a.Hq - a.Hk)) * a.D + c * 8) =
+            quant8_static(x, vd);
+      continue;
+    }
+    const bool is_q = h < a.Hq;
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+    const uint4 w = is_q ? wq : wk;
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    float y[8], z[8], ss = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int hh = h + u;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (hh < h1 && live) {
-        const uint16_t* p = hh < a.Hq          ? a.q + t * a.ld_q + (int64_t)hh * a.D
-                            : hh < a.Hq + a.Hk ? a.k + t * a.ld_k + (int64_t)(hh - a.Hq) * a.D
-                                               : a.v + t * a.ld_v +
-                                                     (int64_t)(hh - a.Hq - a.Hk) * a.D;
-        x[u] = *reinterpret_cast<const uint4*>(p + c * 8);
-      }
+    for (int e = 0; e < 8; ++e) {
+      y[e] = (e & 1) ? bf16_hi(xw[e / 2]) : bf16_lo(xw[e / 2]);
+      ss = __builtin_fmaf(y[e], y[e], ss);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int hh = h + u;
-      if (hh >= h1) break;
-      if (hh >= a.Hq + a.Hk) {                      // a value head: stored as it is
-        if (keep && live) {
-          const int64_t off = (slot * a.Hk + (hh - a.Hq - a.Hk)) * a.D + c * 8;
-          *reinterpret_cast<uint2*>(a.vc + off) = quant8_static(x[u], vd);
-        }
-        continue;
-      }
-      const bool is_q = hh < a.Hq;
-      const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      const uint4 w = is_q ? wq : wk;
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-      float y[8], ss = 0.0f;
+    for (int m = 1; m < L; m <<= 1) ss += __shfl_xor(ss, m);
+    const float r = rsqrt_of(__builtin_fmaf(ss, inv_d, a.eps));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = (e & 1) ? bf16_hi(xw[e / 2]) : bf16_lo(xw[e / 2]);
-        ss = __builtin_fmaf(y[e], y[e], ss);
-      }
+    for (int e = 0; e < 8; ++e)
+      y[e] = y[e] * r * ((e & 1) ? bf16_hi(ww[e / 2]) : bf16_lo(ww[e / 2]));
 #pragma unroll
-      for (int m = 1; m < L; m <<= 1) ss += __shfl_xor(ss, m);
-      const float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(ss, inv_d, a.eps));
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        y[e] = y[e] * r * ((e & 1) ? bf16_hi(ww[e / 2]) : bf16_lo(ww[e / 2]));
-      float z[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // the pair's other value: next to it, or in the partner's lane
-        const float o = kInterleaved ? y[e ^ 1] : __shfl(y[e], lane_base + partner);
-        z[e] = turns ? __builtin_fmaf(o, sn[e], y[e] * cs[e]) : y[e];
-      }
-      if (!live) continue;
-      if (is_q) {
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = bf16_rne(z[2 * e]) | (bf16_rne(z[2 * e + 1]) << 16);
-        *reinterpret_cast<uint4*>(a.q_out + t * a.ld_qo + (int64_t)hh * a.D + c * 8) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-      } else if (keep) {
-        uint32_t o[2] = {0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          o[e / 4] |= (uint32_t)e4m3_encode_one(z[e] / k_scale) << (8 * (e & 3));
-        const int64_t off = (slot * a.Hk + (hh - a.Hq)) * a.D + c * 8;
-        *reinterpret_cast<uint2*>(a.kc + off) = make_uint2(o[0], o[1]);
-      }
+    for (int e = 0; e < 8; ++e) {
+      // the pair's other value: next to it, or in the partner's lane
+      const float o = kInterleaved ? y[e ^ 1] : __shfl(y[e], partner_lane);
+      z[e] = turns ? __builtin_fmaf(o, sn[e], y[e] * cs[e]) : y[e];
     }
+    if (!live) continue;
+    if (is_q)
+      *reinterpret_cast<uint4*>(a.q_out + t * a.ld_qo + (int64_t)h * a.D + c * 8) =
+          make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]),
+                     pack_bf16(z[6], z[7]));
+    else if (keep)
+      *reinterpret_cast<uint2*>(a.kc + (slot * a.Hk + (h - a.Hq)) * a.D + c * 8) =
+          quant8_f32(z, kd);
   }
 }
 
@@ -163,12 +189,13 @@ int lanes_of(int64_t D) {
 }
 
 // Heads per lane group: one while the step is small (latency: every head of
-// every token at once), more when there are tokens enough to fill the card,
-// so that a token's angles are read for several heads.
+// every token at once), up to six while three waves per SIMD are left, so that
+// a token's angles are read for several heads.  8191 tokens of 48 heads of 128
+// take 50 us with 2, 42.4 with 6, 45.7 with 12.
 int heads_per_group(int64_t T, int heads, int L) {
   const int64_t lanes = T * heads * L;
-  for (int per = 8; per > 1; per /= 2)
-    if (lanes / per >= (int64_t)256 * 2048) return per;
+  for (int per : {6, 4, 3, 2})
+    if (lanes / per >= (int64_t)256 * 4 * 3 * 64) return per;
   return 1;
 }
 
@@ -180,9 +207,9 @@ void launch_l(const NormRopeArgs& a, bool inter, hipStream_t st) {
   const int64_t items = a.T * chunks * L;
   const dim3 grid((uint32_t)((items + 255) / 256));
   if (inter)
-    hipLaunchKernelGGL((norm_rope_kernel<L, true>), grid, dim3(256), 0, st, a, per, chunks);
+    hipLaunchKernelGGL((norm_rope_kernel<L, true>), grid, dim3(256), 0, st, a, chunks);
   else
-    hipLaunchKernelGGL((norm_rope_kernel<L, false>), grid, dim3(256), 0, st, a, per, chunks);
+    hipLaunchKernelGGL((norm_rope_kernel<L, false>), grid, dim3(256), 0, st, a, chunks);
 }
 
 }  // namespace
