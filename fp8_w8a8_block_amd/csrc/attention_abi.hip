@@ -314,6 +314,8 @@ fp8_status attention(const uint16_t* query, int64_t ld_query, const uint8_t* key
   a.Hq = (int32_t)Hq;
   a.Hk = (int32_t)Hk;
   a.G = (int32_t)(Hq / Hk);
+  a.inv_G = 1.0 / (double)a.G;
+  a.inv_page = 1.0 / (double)a.page;
   a.ws = (uint8_t*)workspace;
   return launched(fp8k::launch_attention(a, (int)D, (hipStream_t)stream));
 }

@@ -77,6 +77,16 @@ struct Parts {
   float* whole_o;      // [T * Hq][D]
 };
 
+// ---- division -------------------------------------------------------------------
+// x / d for x < 2^51, inv = 1 / d: (x + 1/2) / d lies at least 1 / (2 d) from a
+// whole number, the fp64 error is below x / d * 2^-51.
+__device__ __forceinline__ uint32_t div32(uint32_t x, double inv) {
+  return (uint32_t)__builtin_fma((double)x, inv, 0.5 * inv);
+}
+__device__ __forceinline__ int64_t div64(int64_t x, double inv) {
+  return (int64_t)__builtin_fma((double)x, inv, 0.5 * inv);
+}
+
 // ---- which keys a row tile needs ------------------------------------------------
 struct Request {
   int token0, n;       // first query token, query tokens
@@ -122,7 +132,7 @@ __device__ __forceinline__ Request load_request(const AttentionArgs& a, int r) {
 }
 
 __device__ __forceinline__ int row_tiles(const AttentionArgs& a, const Request& q, int R) {
-  return (int)(((int64_t)q.n * a.G + R - 1) / R);
+  return (int)(((uint32_t)q.n * (uint32_t)a.G + (R - 1)) / R);   // below 2^31 rows
 }
 
 template <bool kPrefix, int R, int KT>
@@ -131,13 +141,13 @@ __device__ __forceinline__ Tiles tiles_of(const AttentionArgs& a, const Request&
   if (kPrefix) {
     t.p_lo = t.p_hi = q.keys - 1;
     t.sink = t.first = 0;
-    t.last = (q.keys + KT - 1) / KT;
+    t.last = (int)(((uint32_t)q.keys + (KT - 1)) / KT);
     return t;
   }
-  const int64_t row = (int64_t)m * R;
-  const int i_lo = (int)(row / a.G);
-  const int64_t i_end = (row + R - 1) / a.G;
-  const int i_hi = i_end < q.n - 1 ? (int)i_end : q.n - 1;
+  const uint32_t row = (uint32_t)m * R;
+  const int i_lo = (int)div32(row, a.inv_G);
+  const int i_end = (int)div32(row + R - 1, a.inv_G);
+  const int i_hi = i_end < q.n - 1 ? i_end : q.n - 1;
   t.p_lo = q.p0 + i_lo;
   t.p_hi = q.p0 + i_hi;
   const int hi = t.p_hi + 1 < q.keys ? t.p_hi + 1 : q.keys;
@@ -145,11 +155,11 @@ __device__ __forceinline__ Tiles tiles_of(const AttentionArgs& a, const Request&
     t.sink = t.first = t.last = 0;
     return t;
   }
-  t.last = (int)(((int64_t)hi + KT - 1) / KT);
+  t.last = (int)(((uint32_t)hi + (KT - 1)) / KT);
   const int low = a.window > 0 && t.p_lo >= a.window ? t.p_lo - a.window + 1 : 0;
   t.first = low / KT < t.last ? low / KT : t.last;
   const int sink_end = a.sinks < hi ? a.sinks : hi;
-  const int st = (int)(((int64_t)sink_end + KT - 1) / KT);
+  const int st = (int)(((uint32_t)sink_end + (KT - 1)) / KT);
   t.sink = st < t.first ? st : t.first;
   return t;
 }
@@ -165,15 +175,20 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// exclusive prefix of v over the workgroup; total in `all`
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_wave, int64_t& all) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t x = v;
+__device__ __forceinline__ int64_t wave_scan(int64_t x) {   // inclusive
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int64_t u = __shfl_up(x, d);
     if (lane >= d) x += u;
   }
+  return x;
+}
+
+// exclusive prefix of v over the workgroup; total in `all`
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_wave, int64_t& all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t x = wave_scan(v);
   __syncthreads();
   if (lane == 63) s_wave[wave] = x;
   __syncthreads();
@@ -187,21 +202,41 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_wave, int64_
   return before + x - v;
 }
 
+// Tiles of all row tiles of request r (0 behind the last), one request per
+// lane.  A lane sums up to 4 row tiles itself; longer requests are taken one by
+// one by the whole wave.
 template <bool kPrefix, int R, int KT>
-__device__ __forceinline__ int64_t request_cost(const AttentionArgs& a, int r) {
-  const Request q = load_request<kPrefix>(a, r);
-  const int mt = row_tiles(a, q, R);
+__device__ __forceinline__ int64_t request_cost(const AttentionArgs& a, int r, int B) {
+  Request q = {};
+  if (r < B) q = load_request<kPrefix>(a, r);
+  const int mt = r < B ? row_tiles(a, q, R) : 0;
   int64_t c = 0;
   if (kPrefix) {
     if (mt > 0) c = (int64_t)mt * cost_of(tiles_of<kPrefix, R, KT>(a, q, 0));
-  } else {
+    return c * a.Hk;
+  }
+  if (mt <= 4)
     for (int m = 0; m < mt; ++m) c += cost_of(tiles_of<kPrefix, R, KT>(a, q, m));
+  for (uint64_t rest = __ballot(mt > 4); rest != 0ull; rest &= rest - 1) {
+    const int of = __ffsll((unsigned long long)rest) - 1;
+    Request x;
+    x.token0 = 0;
+    x.n = uniform(__shfl(q.n, of));
+    x.p0 = uniform(__shfl(q.p0, of));
+    x.keys = uniform(__shfl(q.keys, of));
+    const int xt = uniform(__shfl(mt, of)), lane = threadIdx.x & 63;
+    int64_t part = 0;
+    for (int m = lane; m < xt; m += 64) part += cost_of(tiles_of<kPrefix, R, KT>(a, x, m));
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) part += __shfl_xor(part, d);
+    if (lane == of) c = part;
   }
   return c * a.Hk;
 }
 
 struct Place {
   int64_t share, pos, end;   // tiles per workgroup, this one's range
+  double inv_share;
   int r, m, h, k;            // where pos is
 };
 
@@ -216,8 +251,7 @@ __device__ __forceinline__ Place find_share(const AttentionArgs& a, int wg, int 
   // with at most one request per thread the first pass's scan is kept
   int64_t first_cost = 0, first_before = 0;
   for (int r0 = 0; r0 < B; r0 += kThreads) {
-    const int r = r0 + tid;
-    const int64_t c = r < B ? request_cost<kPrefix, R, KT>(a, r) : 0;
+    const int64_t c = request_cost<kPrefix, R, KT>(a, r0 + tid, B);
     int64_t all;
     const int64_t before = block_scan(c, s_wave, all);
     if (r0 == 0) {
@@ -226,22 +260,22 @@ __device__ __forceinline__ Place find_share(const AttentionArgs& a, int wg, int 
     }
     total += all;
   }
-  p.share = (total + wgs - 1) / wgs;
+  p.share = div64(total + wgs - 1, 1.0 / (double)wgs);
+  p.inv_share = 1.0 / (double)(p.share > 0 ? p.share : 1);
   p.pos = p.share * wg;
   p.end = p.pos + p.share < total ? p.pos + p.share : total;
   p.r = p.m = p.h = p.k = 0;
   if (p.pos >= p.end) return p;
   int64_t base = 0;
   for (int r0 = 0; r0 < B; r0 += kThreads) {
-    const int r = r0 + tid;
     int64_t c = first_cost, before = first_before, all = total;
     if (B > kThreads) {
-      c = r < B ? request_cost<kPrefix, R, KT>(a, r) : 0;
+      c = request_cost<kPrefix, R, KT>(a, r0 + tid, B);
       before = block_scan(c, s_wave, all);
     }
     const int64_t x = p.pos - base - before;
     if (x >= 0 && x < c) {          // one thread of one pass
-      s_found[0] = r;
+      s_found[0] = r0 + tid;
       s_found[1] = x;
     }
     base += all;
@@ -251,34 +285,44 @@ __device__ __forceinline__ Place find_share(const AttentionArgs& a, int wg, int 
   p.r = uniform((int)s_found[0]);
   int64_t x = s_found[1];
   const Request q = load_request<kPrefix>(a, p.r);
+  int64_t c = 1;
   if (kPrefix) {
-    const int64_t c = cost_of(tiles_of<kPrefix, R, KT>(a, q, 0));
-    p.m = uniform((int)(x / (c * a.Hk)));
+    c = cost_of(tiles_of<kPrefix, R, KT>(a, q, 0));
+    p.m = uniform((int)div64(x, 1.0 / (double)(c * a.Hk)));
     x -= (int64_t)p.m * c * a.Hk;
-    p.h = uniform((int)(x / c));
-    p.k = uniform((int)(x - p.h * c));
-    return p;
-  }
-  for (int m = 0;; ++m) {
-    const int64_t c = cost_of(tiles_of<kPrefix, R, KT>(a, q, m));
-    if (x < c * a.Hk) {
-      p.m = uniform(m);
-      p.h = uniform((int)(x / c));
-      p.k = uniform((int)(x - p.h * c));
-      return p;
+  } else {
+    const int mt = row_tiles(a, q, R), lane = tid & 63;
+    for (int m0 = 0; m0 < mt; m0 += 64) {           // every wave alike
+      const int m = m0 + lane;
+      const int64_t mine = m < mt ? cost_of(tiles_of<kPrefix, R, KT>(a, q, m)) : 0;
+      const int64_t upto = wave_scan(mine) * a.Hk;
+      const uint64_t beyond = __ballot(x < upto);
+      if (beyond != 0ull) {
+        const int of = __ffsll((unsigned long long)beyond) - 1;
+        c = __shfl(mine, of);
+        x -= __shfl(upto, of) - c * a.Hk;
+        p.m = uniform(m0 + of);
+        break;
+      }
+      x -= __shfl(upto, 63);
     }
-    x -= c * a.Hk;
   }
+  p.h = uniform((int)div64(x, 1.0 / (double)c));
+  p.k = uniform((int)(x - p.h * c));
+  return p;
 }
 
 // ---- paging ----------------------------------------------------------------------
-// Cache slot of key j of a request, -1 where no block is mapped.
-__device__ __forceinline__ int slot_of(const int32_t* table, int j, int keys, int page,
+// The table's entry for key j of a request (-1 behind the keys), and the cache
+// slot that it names, -1 where no block is mapped.  Two steps, so that the load
+// can be under way while other work is done.
+__device__ __forceinline__ int entry_of(const int32_t* table, int j, int keys, double inv_page) {
+  return j < keys ? table[div32((uint32_t)j, inv_page)] : -1;
+}
+__device__ __forceinline__ int slot_of(int entry, int j, int page, double inv_page,
                                        int num_blocks) {
-  if (j >= keys) return -1;
-  const int i = (int)((uint32_t)j / (uint32_t)page);
-  const int b = table[i];
-  return b >= 0 && b < num_blocks ? b * page + (j - i * page) : -1;
+  const int i = (int)div32((uint32_t)j, inv_page);
+  return entry >= 0 && entry < num_blocks ? entry * page + (j - i * page) : -1;
 }
 
 // ---- conversions -----------------------------------------------------------------
@@ -345,9 +389,21 @@ __device__ __forceinline__ float sum_xor16(float x) {
 // (m = -inf) take 0, so that exp2(-inf - 0) = 0 and nothing turns NaN
 __device__ __forceinline__ float base_of(float m) { return m == FP8_NEG_INF ? 0.0f : m; }
 
-// whether a row at position p sees key j (of a mapped page)
-__device__ __forceinline__ bool sees(int j, int p, int window, int sinks) {
-  return j <= p && (window == 0 || p - j < window || j < sinks);
+// The keys that a row sees: lo .. hi and 0 .. sinks - 1 (up to hi).
+struct Sight {
+  int lo, hi, sinks;
+  __device__ __forceinline__ bool sees(int j) const {
+    return (j <= hi) & ((j >= lo) | (j < sinks));
+  }
+};
+template <bool kPrefix>
+__device__ __forceinline__ Sight sight_of(const AttentionArgs& a, const Request& q, int i) {
+  Sight s;
+  s.hi = kPrefix ? q.keys - 1 : q.p0 + i;
+  s.hi = s.hi < q.keys ? s.hi : q.keys - 1;
+  s.lo = !kPrefix && a.window > 0 ? q.p0 + i - a.window + 1 : 0;
+  s.sinks = a.sinks;
+  return s;
 }
 
 // Arguments read again from the kernel's argument segment: what only an item's
@@ -421,7 +477,7 @@ __device__ __forceinline__ Target target_of(const Place& at, int k1, int cost, i
   t.ends = k1 == cost;
   t.whole = t.begins && t.ends;
   t.slot = 2 * wg + (t.begins ? 1 : 0);
-  t.parts = t.whole ? 0 : (int)((at.pos + cost - 1) / at.share) - wg + 1;
+  t.parts = t.whole ? 0 : (int)div64(at.pos + cost - 1, at.inv_share) - wg + 1;
   return t;
 }
 
@@ -550,8 +606,8 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
     const int rows = uniform(rest < R ? rest : R);
 
     // this lane's row: queries of row n, k slices of group g
-    const int i_n = n < rows ? (row0 + n) / a.G : 0;
-    const int p_n = kPrefix ? q.keys - 1 : q.p0 + i_n;
+    const int i_n = n < rows ? (int)div32((uint32_t)(row0 + n), a.inv_G) : 0;
+    const Sight sight = sight_of<kPrefix>(a, q, i_n);
     bf16x8 qf[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) qf[i] = bf16x8{};
@@ -573,22 +629,24 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
       const int32_t* table = kPrefix ? a.prefix_table : a.table + (int64_t)at.r * a.ld_table;
       const uint8_t* kc = a.kc + (int64_t)at.h * D;
       const uint8_t* vc = a.vc + (int64_t)at.h * D;
-      auto slot_at = [&](int k) {
-        return k < kend ? slot_of(table, tl.key_tile(k) * KT + wave * 32 + (lane & 31), q.keys,
-                                  a.page, a.num_blocks)
-                        : -1;
+      auto key_at = [&](int k) { return tl.key_tile(k) * KT + wave * 32 + (lane & 31); };
+      auto entry_at = [&](int k) {
+        return k < kend ? entry_of(table, key_at(k), q.keys, a.inv_page) : -1;
+      };
+      auto slot_at = [&](int k, int entry) {
+        return slot_of(entry, key_at(k), a.page, a.inv_page, a.num_blocks);
       };
       Unit<D> next;
-      int slot = slot_at(at.k), slot_next = slot_at(at.k + 1);
+      int slot = slot_at(at.k, entry_at(at.k)), entry = entry_at(at.k + 1);
       load_unit<D>(next, kc, vc, stride, slot);
 #pragma unroll 1
       for (int k = at.k; k < kend; ++k) {
         Unit<D> now = next;
         const int kb = tl.key_tile(k) * KT + wave * 32;
         const int mine = slot;
-        slot = slot_next;
+        slot = slot_at(k + 1, entry);
+        entry = entry_at(k + 2);
         if (k + 1 < kend) load_unit<D>(next, kc, vc, stride, slot);
-        slot_next = slot_at(k + 2);
         const uint32_t mapped = (uint32_t)__ballot(mine >= 0);
         if (mapped == 0u) continue;                // nothing of these 32 keys is there
         // S^T: keys 16 t + 4 g + i of row n
@@ -610,7 +668,7 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int b = 16 * t + 4 * g + i;
-              const bool v = ((mapped >> b) & 1u) && sees(kb + b, p_n, a.window, a.sinks);
+              const bool v = ((mapped >> b) & 1u) & (uint32_t)sight.sees(kb + b);
               s[t][i] = v ? s[t][i] : FP8_NEG_INF;
             }
           // values that are not there are zeros
@@ -634,7 +692,7 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
 #pragma unroll 1
             for (int b = 0; b < 32; ++b) {
               const int sb = __shfl(mine, b);
-              if (sb >= 0 && sees(kb + b, p_n, a.window, a.sinks)) {
+              if (sb >= 0 && sight.sees(kb + b)) {
                 const uint8_t* p = vc + (uint64_t)(uint32_t)sb * stride + g * (D / 4);
                 if constexpr (D >= 128) {
                   add_nans(nans, p);
@@ -729,7 +787,7 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
         acc[2] = __builtin_fmaf(y.z, f, acc[2]);
         acc[3] = __builtin_fmaf(y.w, f, acc[3]);
       }
-      const int rr = row0 + row, i = rr / a.G;
+      const int rr = row0 + row, i = (int)div32((uint32_t)rr, a.inv_G);
       const int64_t token = q.token0 + i;
       const int head = at.h * a.G + rr - i * a.G;
       const int64_t flat = token * a.Hq + head;
@@ -760,11 +818,13 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
 // ---- many rows: 128-row tiles ----------------------------------------------------
 // One workgroup of 4 waves, 32 rows each; a key tile is 64 keys, staged in LDS
 // once for all waves: K as bf16 [key][D], V as fp16 [d][key], both converted
-// on the way in (two waves take K, two take V, which transpose in registers).
-// While a tile is multiplied the next one's codes are on their way to
-// registers; they are converted into the other LDS buffer behind the products,
-// so a tile costs one barrier.  32 x 32 x 16 products: lane (n, g) with
-// n = lane % 32 holds row n of S^T and O^T.
+// on the way in (V transposed in registers, 4 keys at a time).  While a tile is
+// multiplied the next one's codes are on their way to registers; they are
+// converted into the other LDS buffer behind the products, so a tile costs one
+// barrier.  32 x 32 x 16 products: lane (n, g) with n = lane % 32 holds row n of
+// S^T and O^T.  The exponents' base m moves only where a row's maximum passes
+// it by 2^8 (P then reaches 256, which fp16 holds as exactly as 1), so that O is
+// rescaled a few times per item and not in every other tile.
 //
 // LDS rows are cut into 16-byte pieces whose index is XORed with the row's, so
 // that the 32 rows that one read names lie in different banks.  O^T's rows
@@ -779,7 +839,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_ker
   constexpr int R = kRowsT, KT = kKeysT;
   constexpr int KS = D / 16;                       // k steps of K Q^T
   constexpr int OB = D / 32;                       // 32-row blocks of O^T
-  constexpr int RAW = D / 8;                       // dwords of codes a thread stages
+  constexpr int RAW = D / 16;                      // dwords of K and of V a thread stages
+  constexpr int VW = D / 64;                       // dwords of a V row that a thread takes
   constexpr int kBuf = KT * D * 2;                 // bytes of a K or V buffer
   constexpr int kPieces = D / 8 < 16 ? D / 8 - 1 : 15;   // K's XOR range
   __shared__ __attribute__((aligned(16))) uint8_t s_kv[4 * kBuf];   // K0 K1 V0 V1
@@ -820,8 +881,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_ker
 
     const int row = wave * 32 + n;                 // this lane's row of the tile
     const bool mine = row < rows;
-    const int i_n = mine ? (row0 + row) / a.G : 0;
-    const int p_n = kPrefix ? q.keys - 1 : q.p0 + i_n;
+    const int i_n = mine ? (int)div32((uint32_t)(row0 + row), a.inv_G) : 0;
+    const Sight sight = sight_of<kPrefix>(a, q, i_n);
     bf16x8 qf[KS];
 #pragma unroll
     for (int i = 0; i < KS; ++i) qf[i] = bf16x8{};
@@ -831,135 +892,152 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_ker
 #pragma unroll
       for (int i = 0; i < KS; ++i) qf[i] = load_query(p + 16 * i, fac.flip);
     }
-    float m = FP8_NEG_INF, l = 0.0f;
-    f32x16 o[OB];
-#pragma unroll
-    for (int b = 0; b < OB; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
-    NanBits<D / 64> nans = {};                     // of this lane's D / 2 values
-
+    const int32_t* table = kPrefix ? a.prefix_table : a.table + (int64_t)at.r * a.ld_table;
+    const uint8_t* kc = a.kc + (int64_t)at.h * D;
+    const uint8_t* vc = a.vc + (int64_t)at.h * D;
     const int count = tl.count();
     const int kend = k1 < count ? k1 : count;
-    if (at.k < kend) {
-      const int32_t* table = kPrefix ? a.prefix_table : a.table + (int64_t)at.r * a.ld_table;
-      const uint8_t* kc = a.kc + (int64_t)at.h * D;
-      const uint8_t* vc = a.vc + (int64_t)at.h * D;
-      uint32_t raw[RAW];
-      auto find_slots = [&](int k) {               // wave 0, one key a lane
-        return k < kend ? slot_of(table, tl.key_tile(k) * KT + lane, q.keys, a.page, a.num_blocks)
-                        : -1;
+    float m, l;
+    f32x16 o[OB];
+    NanBits<D / 64> nans;                          // of this lane's D / 2 values
+
+    // A NaN code among the values makes O NaN in every row of the tile, also in
+    // rows that do not see it.  That is found at the end, and the item is then
+    // done again with the values' codes looked at: NaNs enter as zeros, and the
+    // rows that see them note which.
+    for (bool careful = false;; careful = true) {
+      m = FP8_NEG_INF;
+      l = 0.0f;
+      nans = {};
+#pragma unroll
+      for (int b = 0; b < OB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
+      uint32_t raw_k[RAW], raw_v[RAW];
+      auto entry_at = [&](int k) {                 // wave 0, one key a lane
+        return k < kend ? entry_of(table, tl.key_tile(k) * KT + lane, q.keys, a.inv_page) : -1;
       };
-      auto fetch = [&](int sb) {                   // codes of a tile to registers
-        if (tid < 128) {
-          const int s = s_slot[sb][tid >> 1];
+      auto slot_at = [&](int k, int entry) {
+        return slot_of(entry, tl.key_tile(k) * KT + lane, a.page, a.inv_page, a.num_blocks);
+      };
+      // Codes of a tile to registers: D / 4 bytes of one key, D / 16 bytes of
+      // four keys' values.  Thread t: key t / 4; value columns (t % 16) D / 16 ..
+      // of keys first_v(t) .. + 3, which are half a 16-byte piece of V rows.
+      auto first_v = [](int t) { return (t >> 6) * 16 + ((t >> 5) & 1) * 4 + ((t >> 4) & 1) * 8; };
+      auto fetch = [&](int sb, int t) {
+        const int sk = s_slot[sb][t >> 2];
+        const int4 sv = *reinterpret_cast<const int4*>(&s_slot[sb][first_v(t)]);
+        const uint8_t* pk =
+            kc + (uint64_t)(uint32_t)(sk < 0 ? 0 : sk) * stride + (t & 3) * (D / 4);
+#pragma unroll
+        for (int i = 0; i < RAW / 4; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(pk + 16 * i);
+          raw_k[4 * i] = x.x;
+          raw_k[4 * i + 1] = x.y;
+          raw_k[4 * i + 2] = x.z;
+          raw_k[4 * i + 3] = x.w;
+        }
+        const int s4[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
           const uint8_t* p =
-              kc + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride + (tid & 1) * (D / 2);
-#pragma unroll
-          for (int i = 0; i < RAW / 4; ++i) {
-            const uint4 x = *reinterpret_cast<const uint4*>(p + 16 * i);
-            raw[4 * i] = x.x;
-            raw[4 * i + 1] = x.y;
-            raw[4 * i + 2] = x.z;
-            raw[4 * i + 3] = x.w;
-          }
-        } else {
-          const int u = tid - 128, ch = u >> 4, x16 = u & 15;
-          const int k0 = (ch >> 1) * 16 + (ch & 1) * 4;
-          const int4 lo = *reinterpret_cast<const int4*>(&s_slot[sb][k0]);
-          const int4 hi = *reinterpret_cast<const int4*>(&s_slot[sb][k0 + 8]);
-          const int s8[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint8_t* p =
-                vc + (uint64_t)(uint32_t)(s8[e] < 0 ? 0 : s8[e]) * stride + x16 * (D / 16);
-            if constexpr (D == 64) {
-              raw[e] = *reinterpret_cast<const uint32_t*>(p);
-            } else if constexpr (D == 128) {
-              const uint2 x = *reinterpret_cast<const uint2*>(p);
-              raw[2 * e] = x.x;
-              raw[2 * e + 1] = x.y;
-            } else {
-              const uint4 x = *reinterpret_cast<const uint4*>(p);
-              raw[4 * e] = x.x;
-              raw[4 * e + 1] = x.y;
-              raw[4 * e + 2] = x.z;
-              raw[4 * e + 3] = x.w;
-            }
+              vc + (uint64_t)(uint32_t)(s4[e] < 0 ? 0 : s4[e]) * stride + (t & 15) * (D / 16);
+          if constexpr (D == 64) {
+            raw_v[e] = *reinterpret_cast<const uint32_t*>(p);
+          } else if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            raw_v[2 * e] = x.x;
+            raw_v[2 * e + 1] = x.y;
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(p);
+            raw_v[4 * e] = x.x;
+            raw_v[4 * e + 1] = x.y;
+            raw_v[4 * e + 2] = x.z;
+            raw_v[4 * e + 3] = x.w;
           }
         }
       };
-      auto stage = [&](int buf, int sb, int id) {     // converted into LDS
-        if (tid < 128) {
-          const int key = tid >> 1, p0 = (tid & 1) * (D / 16);
-          uint8_t* dst = s_kv + buf * kBuf + key * (2 * D);
+      // The codes converted into LDS buffer buf.  gaps: some of the tile's keys
+      // are not there.
+      auto stage = [&](int buf, int sb, int id, bool gaps, int t) {
+        {
+          const int key = t >> 2, p0 = (t & 3) * (D / 32);
+          const uint32_t at_k = buf * kBuf + key * (2 * D) + (p0 ^ (key & kPieces)) * 16;
 #pragma unroll
-          for (int i = 0; i < RAW / 2; ++i)
-            *reinterpret_cast<bf16x8*>(dst + (((p0 + i) ^ (key & kPieces)) * 16)) =
-                bf16_of_codes(raw[2 * i], raw[2 * i + 1]);
-        } else {
-          const int u = tid - 128, ch = u >> 4, x16 = u & 15;
-          const int k0 = (ch >> 1) * 16 + (ch & 1) * 4;
-          uint8_t* dst = s_kv + (2 + buf) * kBuf;
+          for (int i = 0; i < D / 32; ++i)
+            *reinterpret_cast<bf16x8*>(s_kv + (at_k ^ (16 * i))) =
+                bf16_of_codes(raw_k[2 * i], raw_k[2 * i + 1]);
+        }
+        if (gaps) {                                // zeros, whatever the address held
+          const int4 sv = *reinterpret_cast<const int4*>(&s_slot[sb][first_v(t)]);
+          const int s4[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int w = 0; w < VW; ++w) raw_v[e * VW + w] = s4[e] < 0 ? 0u : raw_v[e * VW + w];
+        }
+        if (careful) {
           uint32_t nan = 0u;
-          // keys that are not there: zeros, whatever their address held
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const bool there = s_slot[sb][k0 + (e < 4 ? e : e + 4)] >= 0;
+          for (int i = 0; i < RAW; ++i) nan |= nan_codes(raw_v[i]);
+          if (nan != 0u) s_nan[buf] = id;
 #pragma unroll
-            for (int w = 0; w < D / 64; ++w) {
-              raw[e * (D / 64) + w] = there ? raw[e * (D / 64) + w] : 0u;
-              nan |= nan_codes(raw[e * (D / 64) + w]);
-            }
-          }
-          if (nan != 0u) {                         // zeros here; the tile's rows look again
-            s_nan[buf] = id;
+          for (int i = 0; i < RAW; ++i) raw_v[i] = without_nans(raw_v[i]);
+        }
+        // V row of column e: see the order of O^T's rows above; with
+        // x = t % 16 and first row r0, it is r0 + 8 (e / 4) + e % 4, and its
+        // piece's index XORs e / 4 and e % 4
+        const int x = t & 15, rem = x * (D / 16) % (D / 2);
+        const int r0 = (rem / 16) * 32 + ((rem / 4) % 4) * 8 + (x >> 3) * 4;
+        const int piece = ((t >> 5) ^ r0 ^ (r0 >> 3)) & 7;
+        const uint32_t at_v = (2 + buf) * kBuf + r0 * 128 + piece * 16 + ((t >> 4) & 1) * 8;
 #pragma unroll
-            for (int i = 0; i < RAW; ++i) raw[i] = without_nans(raw[i]);
-          }
+        for (int w = 0; w < VW; ++w) {
+          uint32_t col[4];
+          transpose4(raw_v[w], raw_v[VW + w], raw_v[2 * VW + w], raw_v[3 * VW + w], col);
 #pragma unroll
-          for (int w = 0; w < D / 64; ++w) {
-            uint32_t col[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) col[e] = raw[e * (D / 64) + w];
-            f16x8 vo[4];
-            v_operands(col, vo);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const int d = x16 * (D / 16) + 4 * w + b;
-              const int half = d / (D / 2), rem = d % (D / 2);
-              const int vr = (rem / 16) * 32 + ((rem / 4) % 4) * 8 + half * 4 + rem % 4;
-              *reinterpret_cast<f16x8*>(dst + vr * 128 + ((ch ^ vr ^ (vr >> 3)) & 7) * 16) = vo[b];
-            }
+          for (int b = 0; b < 4; ++b) {            // column e = 4 w + b
+            const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(col[b], 1.0f, false);
+            const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(col[b], 1.0f, true);
+            *reinterpret_cast<uint2*>(s_kv + (at_v ^ (16 * (w ^ b))) + (8 * w + b) * 128) =
+                make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
           }
         }
       };
 
       // slots of tiles k and k + 1, the codes of tile k in LDS
-      if (wave == 0) {
-        s_slot[0][lane] = find_slots(at.k);
-        s_slot[1][lane] = find_slots(at.k + 1);
+      if (at.k < kend) {
+        if (wave == 0) {
+          s_slot[0][lane] = slot_at(at.k, entry_at(at.k));
+          s_slot[1][lane] = slot_at(at.k + 1, entry_at(at.k + 1));
+        }
+        __syncthreads();
+        fetch(0, tid);
+        stage(0, 0, serial, __ballot(s_slot[0][lane] >= 0) != ~0ull, tid);
+        __syncthreads();
       }
-      __syncthreads();
       int cur = 0, s0 = 0, s1 = 1, s2 = 2;
-      fetch(0);
-      stage(0, 0, serial);
-      __syncthreads();
 #pragma unroll 1
       for (int k = at.k; k < kend; ++k) {
+        // addresses are formed in each pass from here: kept through the loop
+        // they would take the registers that the products' operands need
+        int t_ = tid, n_ = n, g_ = g;
+        asm volatile("" : "+v"(t_), "+v"(n_), "+v"(g_));
         const int kb = tl.key_tile(k) * KT;
-        const uint64_t mapped = __ballot(s_slot[s0][lane] >= 0);
+        // the table's entries first: waiting for them later leaves the codes
+        // behind them in flight
+        int entry = -1;
+        if (wave == 0) entry = entry_at(k + 2);
+        const uint64_t mapped = __ballot((s_slot[s0][lane] >= 0) | (kb + lane >= q.keys));
         const bool more = k + 1 < kend;
-        if (more) fetch(s1);
-        int next_slot = -1;
-        if (wave == 0) next_slot = find_slots(k + 2);
+        const bool gaps = __ballot(s_slot[s1][lane] >= 0) != ~0ull;
+        if (more) fetch(s1, t_);
 
         // S^T: block t holds keys 32 t + 8 (v / 4) + 4 g + v % 4 of row n
         f32x16 s[2];
         {
-          int piece = (g ^ (n & kPieces)) * 16;    // of k step 0; step i XORs 32 i
-          asm volatile("" : "+v"(piece));          // computed per read, not kept
-          const uint8_t* kr = s_kv + cur * kBuf + n * (2 * D);
+          // piece of k step 0; step i XORs 2 i
+          const uint32_t at_k = cur * kBuf + n_ * (2 * D) + (g_ ^ (n_ & kPieces)) * 16;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -967,29 +1045,34 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_ker
 #pragma unroll
             for (int i = 0; i < KS; ++i)
               s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                  *reinterpret_cast<const bf16x8*>(kr + t * (64 * D) + (piece ^ (32 * i))), qf[i],
+                  *reinterpret_cast<const bf16x8*>(s_kv + (at_k ^ (32 * i)) + t * (64 * D)), qf[i],
                   s[t], 0, 0, 0);
           }
         }
         const int last = kb + KT - 1;
-        const bool all = mapped == ~0ull && last <= tl.p_lo &&
+        const bool all = mapped == ~0ull && last <= (kPrefix ? q.keys - 1 : tl.p_lo) &&
                          (a.window == 0 || tl.p_hi - kb < a.window || last < a.sinks);
         if (!all) {
+          // of the lane's keys, relative to kb + 4 g
+          const int hi = sight.hi - kb - 4 * g_, lo = sight.lo - kb - 4 * g_;
+          const int sk = sight.sinks - kb - 4 * g_;
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2; ++t) {
+            const uint32_t there = (uint32_t)(mapped >> (32 * t)) >> (4 * g_);
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
-              const int b = 32 * t + 8 * (v / 4) + 4 * g + v % 4;
-              const bool is = ((mapped >> b) & 1u) && sees(kb + b, p_n, a.window, a.sinks);
+              const int b = 8 * (v / 4) + v % 4, j = 32 * t + b;
+              const bool is = (j <= hi) & ((j >= lo) | (j < sk)) & (((there >> b) & 1u) != 0u);
               s[t][v] = is ? s[t][v] : FP8_NEG_INF;
             }
+          }
         }
-        if (s_nan[cur] == serial) {                // NaN values: which ones does this row see?
+        if (careful && s_nan[cur] == serial) {     // NaN values: which ones does this row see?
 #pragma unroll 1
           for (int b = 0; b < KT; ++b) {
             const int sb = s_slot[s0][b];
-            if (sb >= 0 && sees(kb + b, p_n, a.window, a.sinks))
-              add_nans(nans, vc + (uint64_t)(uint32_t)sb * stride + g * (D / 2));
+            if (sb >= 0 && sight.sees(kb + b))
+              add_nans(nans, vc + (uint64_t)(uint32_t)sb * stride + g_ * (D / 2));
           }
         }
         float top = s[0][0];
@@ -998,10 +1081,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_ker
 #pragma unroll
           for (int v = 0; v < 16; ++v) top = __builtin_fmaxf(top, s[t][v]);
         top = max_xor32(top) * c;
-        const float m_new = __builtin_fmaxf(m, top);
-        const float base = base_of(m_new);
-        if (__ballot(m_new != m) != 0ull) {        // some row's maximum grew
-          const float alpha = __builtin_amdgcn_exp2f(m - base);
+        if (__ballot(top > m + 8.0f) != 0ull) {    // some row's maximum grew out of reach
+          const float m_new = __builtin_fmaxf(m, top);
+          const float alpha = __builtin_amdgcn_exp2f(m - base_of(m_new));
           l *= alpha;
 #pragma unroll
           for (int b = 0; b < OB; ++b)
@@ -1009,6 +1091,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_ker
             for (int i = 0; i < 16; ++i) o[b][i] *= alpha;
           m = m_new;
         }
+        const float base = base_of(m);
         float sum = 0.0f;
         f16x8 p[4];
 #pragma unroll
@@ -1021,21 +1104,20 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_ker
           }
         l += sum;
         {
-          int piece = ((g ^ n ^ (n >> 3)) & 7) * 16;   // of row n, k step 0
-          asm volatile("" : "+v"(piece));
-          const uint8_t* vr = s_kv + (2 + cur) * kBuf + n * 128;
+          const uint32_t at_v =
+              (2 + cur) * kBuf + n_ * 128 + ((g_ ^ n_ ^ (n_ >> 3)) & 7) * 16;
 #pragma unroll
           for (int b = 0; b < OB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                  *reinterpret_cast<const f16x8*>(vr + b * 4096 +
-                                                  (piece ^ (32 * i) ^ ((b & 1) * 64))),
+                  *reinterpret_cast<const f16x8*>(s_kv + (at_v ^ (32 * i) ^ (64 * (b & 1))) +
+                                                  b * 4096),
                   p[i], o[b], 0, 0, 0);
         }
         ++serial;
-        if (more) stage(cur ^ 1, s1, serial);
-        if (wave == 0) s_slot[s2][lane] = next_slot;   // tile k - 1's place
+        if (more) stage(cur ^ 1, s1, serial, gaps, t_);
+        if (wave == 0) s_slot[s2][lane] = slot_at(k + 2, entry);   // tile k - 1's place
         __syncthreads();
         cur ^= 1;
         const int done = s0;
@@ -1043,6 +1125,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_ker
         s1 = s2;
         s2 = done;
       }
+      if (careful) break;
+      bool bad = false;
+#pragma unroll
+      for (int b = 0; b < OB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bad |= o[b][i] != o[b][i];
+      if (!__syncthreads_or(bad)) break;
     }
     l = sum_xor32(l);
 
@@ -1193,7 +1282,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
         for (int i = 0; i < D / 64; ++i) s.o[i] += s_o[w][lane * (D / 64) + i];
       }
     }
-    const int rho = sp.row0 + row, i = rho / a.G;
+    const int rho = sp.row0 + row, i = (int)div32((uint32_t)rho, a.inv_G);
     write_row<D>(a, s, base, sp.token0 + i, sp.head * a.G + rho - i * a.G);
   }
 }

@@ -75,6 +75,7 @@ struct AttentionArgs {
   int64_t ld_out;
   float* lse;
   int32_t T, Hq, Hk, G;         // G = Hq / Hk
+  double inv_G, inv_page;       // 1 / G, 1 / page
   uint8_t* ws;
 };
 // Workspace bytes of launch_attention for these sizes on the current device.
