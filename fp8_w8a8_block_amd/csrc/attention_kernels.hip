@@ -171,7 +171,7 @@ __device__ __forceinline__ int cost_of(const Tiles& t) {
 }
 
 // ---- shares ----------------------------------------------------------------------
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;     // of the 16-row and the joining kernels
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -185,7 +185,8 @@ __device__ __forceinline__ int64_t wave_scan(int64_t x) {   // inclusive
   return x;
 }
 
-// exclusive prefix of v over the workgroup; total in `all`
+// exclusive prefix of v over the workgroup's kWaves waves; total in `all`
+template <int kWaves>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_wave, int64_t& all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t x = wave_scan(v);
@@ -195,7 +196,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_wave, int64_
   int64_t before = 0;
   all = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     if (w < wave) before += s_wave[w];
     all += s_wave[w];
   }
@@ -241,9 +242,10 @@ struct Place {
 };
 
 // Finds this workgroup's share and where it begins.
-template <bool kPrefix, int R, int KT>
+template <bool kPrefix, int R, int KT, int kWaves>
 __device__ __forceinline__ Place find_share(const AttentionArgs& a, int wg, int wgs,
                                             int64_t* s_wave, int64_t* s_found) {
+  constexpr int kThreads = kWaves * 64;
   const int tid = threadIdx.x;
   const int B = kPrefix ? 1 : a.B;
   Place p;
@@ -253,7 +255,7 @@ __device__ __forceinline__ Place find_share(const AttentionArgs& a, int wg, int 
   for (int r0 = 0; r0 < B; r0 += kThreads) {
     const int64_t c = request_cost<kPrefix, R, KT>(a, r0 + tid, B);
     int64_t all;
-    const int64_t before = block_scan(c, s_wave, all);
+    const int64_t before = block_scan<kWaves>(c, s_wave, all);
     if (r0 == 0) {
       first_cost = c;
       first_before = before;
@@ -271,7 +273,7 @@ __device__ __forceinline__ Place find_share(const AttentionArgs& a, int wg, int 
     int64_t c = first_cost, before = first_before, all = total;
     if (B > kThreads) {
       c = request_cost<kPrefix, R, KT>(a, r0 + tid, B);
-      before = block_scan(c, s_wave, all);
+      before = block_scan<kWaves>(c, s_wave, all);
     }
     const int64_t x = p.pos - base - before;
     if (x >= 0 && x < c) {          // one thread of one pass
@@ -583,7 +585,7 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int wg = blockIdx.x;
-  Place at = find_share<kPrefix, R, KT>(a, wg, gridDim.x, s_wave, s_found);
+  Place at = find_share<kPrefix, R, KT, 4>(a, wg, gridDim.x, s_wave, s_found);
   if (!kJoin && tid == 0) args.parts.split[wg].parts = 0;
   const uint32_t stride = (uint32_t)a.Hk * D;
   const Factor fac = factor_of(a);
@@ -815,53 +817,87 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
   }
 }
 
-// ---- many rows: 128-row tiles ----------------------------------------------------
-// One workgroup of 4 waves, 32 rows each; a key tile is 64 keys, staged in LDS
-// once for all waves: K as bf16 [key][D], V as fp16 [d][key], both converted
-// on the way in (V transposed in registers, 4 keys at a time).  While a tile is
-// multiplied the next one's codes are on their way to registers; they are
-// converted into the other LDS buffer behind the products, so a tile costs one
-// barrier.  32 x 32 x 16 products: lane (n, g) with n = lane % 32 holds row n of
-// S^T and O^T.  The exponents' base m moves only where a row's maximum passes
-// it by 2^8 (P then reaches 256, which fp16 holds as exactly as 1), so that O is
-// rescaled a few times per item and not in every other tile.
+// ---- many rows: 256-row tiles ----------------------------------------------------
+// One workgroup of kWaves waves, 32 rows each; a key tile is 64 keys, staged in
+// LDS once for all waves: K as bf16 [key][D], V as fp16 [d][key], both converted
+// on the way in (V transposed in registers, 4 keys at a time), two buffers each.
+// 32 x 32 x 16 products: lane (n, g) with n = lane % 32 holds row n of S^T and O^T.
+//
+// Two phases alternate: products (V j with P j, then K j + 1 with Q) and softmax
+// (S j to P j).  The waves form two groups half a period apart, a barrier between
+// the phases: while one group keeps a SIMD's matrix unit busy, the other, on the
+// same SIMD, has its vector unit.  A wave issues a vector instruction every 7
+// cycles beside another's products, so what else there is to do stands between
+// the products, 32 cycles each: parts of K j + 2 and V j + 1 go from registers to
+// LDS, and the codes behind them are read.  With j counting tiles, interval i
+// between two barriers holds softmax j of the first group at i = 2 j + 1 and its
+// products j at 2 j + 2, those of the second group one interval later.  K j + 1
+// and V j are then read in 2 j + 2 and 2 j + 3; they were written in the two
+// intervals before, when their buffers' last readers were done.
+//
+// The exponents' base m moves only where a row's maximum passes it by 2^8 (P then
+// reaches 256, which fp16 holds as exactly as 1), so that O is rescaled a few
+// times per item and not in every other tile.
 //
 // LDS rows are cut into 16-byte pieces whose index is XORed with the row's, so
 // that the 32 rows that one read names lie in different banks.  O^T's rows
 // are not d in order: row 32 b + 8 i + 4 g + e is d = g D/2 + 16 b + 4 i + e, which
 // leaves each lane with D / 2 values in a row to store.
-constexpr int kRowsT = 128;
-constexpr int kKeysT = 64;
+constexpr int tile_keys(int D) { return D == 64 ? 128 : 64; }
+
+// waves of a workgroup: D = 256 needs a whole SIMD's registers for one wave
+constexpr int tile_waves(int D) { return D == 256 ? 4 : 8; }
 
 template <int D, bool kPrefix, bool kJoin>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_kernel(
+__global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attention_tile_kernel(
     KernelArgs args) {
-  constexpr int R = kRowsT, KT = kKeysT;
+  constexpr int kWaves = tile_waves(D);
+  constexpr int R = kWaves * 32, KT = tile_keys(D);
   constexpr int KS = D / 16;                       // k steps of K Q^T
   constexpr int OB = D / 32;                       // 32-row blocks of O^T
-  constexpr int RAW = D / 16;                      // dwords of K and of V a thread stages
-  constexpr int VW = D / 64;                       // dwords of a V row that a thread takes
+  constexpr int NB = KT / 32;                      // 32-key blocks of S^T
+  constexpr int kThreads = kWaves * 64;
+  constexpr int TK = kThreads / KT;                // threads of a key's row of K
+  constexpr int TV = kThreads / (KT / 4);          // threads of four keys' rows of V
+  constexpr int KW = D / TK / 4;                   // dwords that one takes of the row of K,
+  constexpr int VW = D / TV / 4;                   // and of each of the rows of V
   constexpr int kBuf = KT * D * 2;                 // bytes of a K or V buffer
   constexpr int kPieces = D / 8 < 16 ? D / 8 - 1 : 15;   // K's XOR range
   __shared__ __attribute__((aligned(16))) uint8_t s_kv[4 * kBuf];   // K0 K1 V0 V1
-  __shared__ __attribute__((aligned(16))) int s_slot[3][KT];   // of tiles k, k + 1 and k + 2
+  __shared__ __attribute__((aligned(16))) int s_slot[8][KT];   // of tile k in s_slot[k % 8]
   __shared__ int s_nan[2];                         // the last tile staged there with a NaN value
-  __shared__ int64_t s_wave[4], s_found[2];
+  __shared__ int64_t s_wave[kWaves], s_found[2];
   const AttentionArgs& a = args.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int n = lane & 31, g = lane >> 5;
+  const bool second = wave >= kWaves / 2;          // group
   // neighbouring shares, which read the same keys, on one XCD (workgroups go
   // round robin over the 8)
   const int wgs = gridDim.x;
   const int wg = wgs % 8 == 0 ? (int)(blockIdx.x % 8) * (wgs / 8) + (int)(blockIdx.x / 8)
                               : (int)blockIdx.x;
-  Place at = find_share<kPrefix, R, KT>(a, wg, wgs, s_wave, s_found);
+  Place at = find_share<kPrefix, R, KT, kWaves>(a, wg, wgs, s_wave, s_found);
   if (!kJoin && tid == 0) args.parts.split[wg].parts = 0;
-  if (tid < 2) s_nan[tid] = -1;
   const uint32_t stride = (uint32_t)a.Hk * D;
   const Factor fac = factor_of(a);
   const float c = fac.c;
-  int serial = 0;                                  // tiles staged so far
+
+  // LDS places of this thread in buffers 0.  Reads: piece of k step 0 of row n of
+  // K and of V; step i XORs 2 i.
+  const uint32_t from_k = n * (2 * D) + (g ^ (n & kPieces)) * 16;
+  const uint32_t from_v = 2 * kBuf + n * (2 * KT) + (g ^ ((n ^ (n >> 3)) & 7)) * 16;
+  // Writes: a thread puts 4 KW codes of key tid / TK, and of column e < 4 VW of
+  // its V columns half a piece, keys first_v .. + 3.  V row of column e: see the
+  // order of O^T's rows above; with first row r0 it is r0 + 32 (e / 16) +
+  // 8 (e / 4 % 4) + e % 4, and its piece's index XORs those too.
+  const int key_k = tid / TK, x_v = tid % TV, y_v = tid / TV;
+  const uint32_t to_k =
+      key_k * (2 * D) + (((tid % TK) * (KW / 2)) ^ (key_k & kPieces)) * 16;
+  const int first_v = (y_v >> 2) * 16 + ((y_v >> 1) & 1) * 4 + (y_v & 1) * 8;
+  const int rem_v = x_v * (4 * VW) % (D / 2);
+  const int r0_v = (rem_v / 16) * 32 + ((rem_v / 4) % 4) * 8 + (x_v / (TV / 2)) * 4;
+  const uint32_t to_v = 2 * kBuf + r0_v * (2 * KT) +
+                        ((y_v >> 1) ^ ((r0_v ^ (r0_v >> 3)) & 7)) * 16 + (y_v & 1) * 8;
 
   while (at.pos < at.end) {
     const Request q = load_request<kPrefix>(a, at.r);
@@ -893,8 +929,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_ker
       for (int i = 0; i < KS; ++i) qf[i] = load_query(p + 16 * i, fac.flip);
     }
     const int32_t* table = kPrefix ? a.prefix_table : a.table + (int64_t)at.r * a.ld_table;
-    const uint8_t* kc = a.kc + (int64_t)at.h * D;
     const uint8_t* vc = a.vc + (int64_t)at.h * D;
+    const uint8_t* codes_k = a.kc + (int64_t)at.h * D + (tid % TK) * (4 * KW);   // this thread's
+    const uint8_t* codes_v = vc + x_v * (4 * VW);
     const int count = tl.count();
     const int kend = k1 < count ? k1 : count;
     float m, l;
@@ -913,63 +950,58 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_ker
       for (int b = 0; b < OB; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
-      uint32_t raw_k[RAW], raw_v[RAW];
-      auto entry_at = [&](int k) {                 // wave 0, one key a lane
-        return k < kend ? entry_of(table, tl.key_tile(k) * KT + lane, q.keys, a.inv_page) : -1;
+      uint32_t raw_k[KW], raw_v[4 * VW];
+      auto entry_at = [&](int k) {                 // a key per lane of the first waves
+        return k < kend ? entry_of(table, tl.key_tile(k) * KT + tid, q.keys, a.inv_page) : -1;
       };
       auto slot_at = [&](int k, int entry) {
-        return slot_of(entry, tl.key_tile(k) * KT + lane, a.page, a.inv_page, a.num_blocks);
+        return slot_of(entry, tl.key_tile(k) * KT + tid, a.page, a.inv_page, a.num_blocks);
       };
-      // Codes of a tile to registers: D / 4 bytes of one key, D / 16 bytes of
-      // four keys' values.  Thread t: key t / 4; value columns (t % 16) D / 16 ..
-      // of keys first_v(t) .. + 3, which are half a 16-byte piece of V rows.
-      auto first_v = [](int t) { return (t >> 6) * 16 + ((t >> 5) & 1) * 4 + ((t >> 4) & 1) * 8; };
-      auto fetch = [&](int sb, int t) {
-        const int sk = s_slot[sb][t >> 2];
-        const int4 sv = *reinterpret_cast<const int4*>(&s_slot[sb][first_v(t)]);
-        const uint8_t* pk =
-            kc + (uint64_t)(uint32_t)(sk < 0 ? 0 : sk) * stride + (t & 3) * (D / 4);
-#pragma unroll
-        for (int i = 0; i < RAW / 4; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(pk + 16 * i);
-          raw_k[4 * i] = x.x;
-          raw_k[4 * i + 1] = x.y;
-          raw_k[4 * i + 2] = x.z;
-          raw_k[4 * i + 3] = x.w;
-        }
-        const int s4[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint8_t* p =
-              vc + (uint64_t)(uint32_t)(s4[e] < 0 ? 0 : s4[e]) * stride + (t & 15) * (D / 16);
-          if constexpr (D == 64) {
-            raw_v[e] = *reinterpret_cast<const uint32_t*>(p);
-          } else if constexpr (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(p);
-            raw_v[2 * e] = x.x;
-            raw_v[2 * e + 1] = x.y;
-          } else {
-            const uint4 x = *reinterpret_cast<const uint4*>(p);
-            raw_v[4 * e] = x.x;
-            raw_v[4 * e + 1] = x.y;
-            raw_v[4 * e + 2] = x.z;
-            raw_v[4 * e + 3] = x.w;
-          }
+      // Codes to registers: part i of a thread's piece of a key, and what it
+      // takes of one of four keys' values.
+      constexpr int kLoads = KW / 4 + 4;
+      auto fetch_k = [&](int i, int slot) {
+        const uint8_t* p = codes_k + (uint64_t)(uint32_t)(slot < 0 ? 0 : slot) * stride;
+        const uint4 x = *reinterpret_cast<const uint4*>(p + 16 * i);
+        raw_k[4 * i] = x.x;
+        raw_k[4 * i + 1] = x.y;
+        raw_k[4 * i + 2] = x.z;
+        raw_k[4 * i + 3] = x.w;
+      };
+      auto fetch_v = [&](int e, const int4& slots) {
+        const int slot = e == 0 ? slots.x : e == 1 ? slots.y : e == 2 ? slots.z : slots.w;
+        const uint8_t* p = codes_v + (uint64_t)(uint32_t)(slot < 0 ? 0 : slot) * stride;
+        if constexpr (VW == 1) {
+          raw_v[e] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+          const uint4 x = *reinterpret_cast<const uint4*>(p);
+          raw_v[4 * e] = x.x;
+          raw_v[4 * e + 1] = x.y;
+          raw_v[4 * e + 2] = x.z;
+          raw_v[4 * e + 3] = x.w;
         }
       };
-      // The codes converted into LDS buffer buf.  gaps: some of the tile's keys
-      // are not there.
-      auto stage = [&](int buf, int sb, int id, bool gaps, int t) {
-        {
-          const int key = t >> 2, p0 = (t & 3) * (D / 32);
-          const uint32_t at_k = buf * kBuf + key * (2 * D) + (p0 ^ (key & kPieces)) * 16;
+      auto slot_k = [&](int k) { return s_slot[k & 7][key_k]; };
+      auto slots_v = [&](int k) {
+        return *reinterpret_cast<const int4*>(&s_slot[k & 7][first_v]);
+      };
+      // Whether all keys of tile k are there; with the keys behind the last one
+      // counted as there, whether any is unmapped.
+      auto mapped_of = [&](int k, bool behind, uint64_t map[NB / 2]) {
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            *reinterpret_cast<bf16x8*>(s_kv + (at_k ^ (16 * i))) =
-                bf16_of_codes(raw_k[2 * i], raw_k[2 * i + 1]);
-        }
-        if (gaps) {                                // zeros, whatever the address held
-          const int4 sv = *reinterpret_cast<const int4*>(&s_slot[sb][first_v(t)]);
+        for (int i = 0; i < NB / 2; ++i)
+          map[i] = __ballot((s_slot[k & 7][64 * i + lane] >= 0) |
+                            (behind & (tl.key_tile(k) * KT + 64 * i + lane >= q.keys)));
+      };
+      // Rare: values of keys that are not there become zeros, whatever the
+      // address held, and a careful pass takes the NaNs out.
+      auto mend_v = [&](int k, int buf) {
+        uint64_t there[NB / 2], every = ~0ull;
+        mapped_of(k, false, there);
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) every &= there[i];
+        if (every != ~0ull) {
+          const int4 sv = slots_v(k);
           const int s4[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -979,151 +1011,225 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_tile_ker
         if (careful) {
           uint32_t nan = 0u;
 #pragma unroll
-          for (int i = 0; i < RAW; ++i) nan |= nan_codes(raw_v[i]);
-          if (nan != 0u) s_nan[buf] = id;
+          for (int i = 0; i < 4 * VW; ++i) nan |= nan_codes(raw_v[i]);
+          if (nan != 0u) s_nan[buf] = k;
 #pragma unroll
-          for (int i = 0; i < RAW; ++i) raw_v[i] = without_nans(raw_v[i]);
-        }
-        // V row of column e: see the order of O^T's rows above; with
-        // x = t % 16 and first row r0, it is r0 + 8 (e / 4) + e % 4, and its
-        // piece's index XORs e / 4 and e % 4
-        const int x = t & 15, rem = x * (D / 16) % (D / 2);
-        const int r0 = (rem / 16) * 32 + ((rem / 4) % 4) * 8 + (x >> 3) * 4;
-        const int piece = ((t >> 5) ^ r0 ^ (r0 >> 3)) & 7;
-        const uint32_t at_v = (2 + buf) * kBuf + r0 * 128 + piece * 16 + ((t >> 4) & 1) * 8;
-#pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          uint32_t col[4];
-          transpose4(raw_v[w], raw_v[VW + w], raw_v[2 * VW + w], raw_v[3 * VW + w], col);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {            // column e = 4 w + b
-            const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(col[b], 1.0f, false);
-            const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(col[b], 1.0f, true);
-            *reinterpret_cast<uint2*>(s_kv + (at_v ^ (16 * (w ^ b))) + (8 * w + b) * 128) =
-                make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
-          }
+          for (int i = 0; i < 4 * VW; ++i) raw_v[i] = without_nans(raw_v[i]);
         }
       };
-
-      // slots of tiles k and k + 1, the codes of tile k in LDS
+      // The codes in registers go to LDS, converted, in small steps u.
+      constexpr int kPutsK = 2 * KW, kPutsV = 10 * VW;
+      uint32_t col[4], half_k[4], half[4];
+      auto put_k = [&](int u, uint32_t to) {        // two codes; 16 bytes every 4 steps
+        const int i = u / 4, j = u % 4;
+        half_k[j] = __builtin_bit_cast(
+            uint32_t,
+            j & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw_k[2 * i + j / 2], 1.0f, true)
+                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw_k[2 * i + j / 2], 1.0f, false));
+        if (j == 3) {
+          *reinterpret_cast<uint4*>(s_kv + (to ^ (16 * i))) =
+              make_uint4(half_k[0], half_k[1], half_k[2], half_k[3]);
+        }
+      };
+      auto put_v = [&](int u, uint32_t to) {        // a dword column of 4 keys in 10 steps
+        const int w = u / 10, j = u % 10;
+        if (j == 0) {
+          half[0] = __builtin_amdgcn_perm(raw_v[VW + w], raw_v[w], 0x05010400u);
+          half[1] = __builtin_amdgcn_perm(raw_v[VW + w], raw_v[w], 0x07030602u);
+          half[2] = __builtin_amdgcn_perm(raw_v[3 * VW + w], raw_v[2 * VW + w], 0x05010400u);
+          half[3] = __builtin_amdgcn_perm(raw_v[3 * VW + w], raw_v[2 * VW + w], 0x07030602u);
+        } else if (j == 1) {
+          col[0] = __builtin_amdgcn_perm(half[2], half[0], 0x05040100u);
+          col[1] = __builtin_amdgcn_perm(half[2], half[0], 0x07060302u);
+          col[2] = __builtin_amdgcn_perm(half[3], half[1], 0x05040100u);
+          col[3] = __builtin_amdgcn_perm(half[3], half[1], 0x07060302u);
+        } else if (j % 2 == 0) {
+          half[0] = __builtin_bit_cast(
+              uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(col[j / 2 - 1], 1.0f, false));
+        } else {
+          const int b = j / 2 - 1;                 // column e = 4 w + b
+          half[1] = __builtin_bit_cast(
+              uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(col[b], 1.0f, true));
+          const int flip = b ^ (w & 3) ^ ((w >> 2) * 4), down = (w >> 2) * 32 + (w & 3) * 8 + b;
+          *reinterpret_cast<uint2*>(s_kv + (to ^ (16 * flip)) + down * (2 * KT)) =
+              make_uint2(half[0], half[1]);
+        }
+      };
       if (at.k < kend) {
-        if (wave == 0) {
-          s_slot[0][lane] = slot_at(at.k, entry_at(at.k));
-          s_slot[1][lane] = slot_at(at.k + 1, entry_at(at.k + 1));
+        if (tid < 2) s_nan[tid] = -1;
+        int entry = -1;                            // of tile k + 3
+        if (wave < NB / 2) {
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            s_slot[(at.k + i) & 7][tid] = slot_at(at.k + i, entry_at(at.k + i));
+          entry = entry_at(at.k + 3);
         }
         __syncthreads();
-        fetch(0, tid);
-        stage(0, 0, serial, __ballot(s_slot[0][lane] >= 0) != ~0ull, tid);
-        __syncthreads();
-      }
-      int cur = 0, s0 = 0, s1 = 1, s2 = 2;
-#pragma unroll 1
-      for (int k = at.k; k < kend; ++k) {
-        // addresses are formed in each pass from here: kept through the loop
-        // they would take the registers that the products' operands need
-        int t_ = tid, n_ = n, g_ = g;
-        asm volatile("" : "+v"(t_), "+v"(n_), "+v"(g_));
-        const int kb = tl.key_tile(k) * KT;
-        // the table's entries first: waiting for them later leaves the codes
-        // behind them in flight
-        int entry = -1;
-        if (wave == 0) entry = entry_at(k + 2);
-        const uint64_t mapped = __ballot((s_slot[s0][lane] >= 0) | (kb + lane >= q.keys));
-        const bool more = k + 1 < kend;
-        const bool gaps = __ballot(s_slot[s1][lane] >= 0) != ~0ull;
-        if (more) fetch(s1, t_);
-
-        // S^T: block t holds keys 32 t + 8 (v / 4) + 4 g + v % 4 of row n
-        f32x16 s[2];
-        {
-          // piece of k step 0; step i XORs 2 i
-          const uint32_t at_k = cur * kBuf + n_ * (2 * D) + (g_ ^ (n_ & kPieces)) * 16;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
+        for (int j = 0; j < 3; ++j) {              // K j to LDS, then K j + 1; V j - 1, V j
+          if (j > 0) {
 #pragma unroll
-            for (int v = 0; v < 16; ++v) s[t][v] = 0.0f;
+            for (int u = 0; u < kPutsK; ++u) put_k(u, to_k + (j - 1) * kBuf);
+          }
+          const int slot = slot_k(at.k + j);
 #pragma unroll
-            for (int i = 0; i < KS; ++i)
-              s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                  *reinterpret_cast<const bf16x8*>(s_kv + (at_k ^ (32 * i)) + t * (64 * D)), qf[i],
-                  s[t], 0, 0, 0);
+          for (int i = 0; i < KW / 4; ++i) fetch_k(i, slot);
+          if (j < 2) {
+            if (j == 1) {
+              mend_v(at.k, 0);
+#pragma unroll
+              for (int u = 0; u < kPutsV; ++u) put_v(u, to_v);
+            }
+            const int4 slots = slots_v(at.k + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) fetch_v(e, slots);
           }
         }
-        const int last = kb + KT - 1;
-        const bool all = mapped == ~0ull && last <= (kPrefix ? q.keys - 1 : tl.p_lo) &&
-                         (a.window == 0 || tl.p_hi - kb < a.window || last < a.sinks);
-        if (!all) {
-          // of the lane's keys, relative to kb + 4 g
-          const int hi = sight.hi - kb - 4 * g_, lo = sight.lo - kb - 4 * g_;
-          const int sk = sight.sinks - kb - 4 * g_;
+        __syncthreads();
+        if (second) __syncthreads();               // half a period behind
+        // S^T: block t holds keys 32 t + 8 (v / 4) + 4 g + v % 4 of row n
+        f32x16 s[NB];
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint32_t there = (uint32_t)(mapped >> (32 * t)) >> (4 * g_);
+        for (int t = 0; t < NB; ++t)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-              const int b = 8 * (v / 4) + v % 4, j = 32 * t + b;
-              const bool is = (j <= hi) & ((j >= lo) | (j < sk)) & (((there >> b) & 1u) != 0u);
-              s[t][v] = is ? s[t][v] : FP8_NEG_INF;
+          for (int v = 0; v < 16; ++v) s[t][v] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int t = 0; t < NB; ++t)
+            s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                *reinterpret_cast<const bf16x8*>(s_kv + (from_k ^ (32 * i)) + t * (64 * D)),
+                qf[i], s[t], 0, 0, 0);
+        __syncthreads();
+        int cur = 0;
+        uint64_t mapped[NB / 2];
+        mapped_of(at.k, true, mapped);
+#pragma unroll 1
+        for (int k = at.k; k < kend; ++k) {
+          // what is formed from these is formed in each pass: kept through the
+          // loop it would take the registers that the products' operands need
+          int g_ = g;
+          uint32_t at_k = from_k, at_v = from_v, put_at_k = to_k, put_at_v = to_v;
+          asm volatile("" : "+v"(g_), "+v"(at_k), "+v"(at_v), "+v"(put_at_k), "+v"(put_at_v));
+          at_k += (cur ^ 1) * kBuf;
+          at_v += cur * kBuf;
+          put_at_k += cur * kBuf;
+          put_at_v += (cur ^ 1) * kBuf;
+          const int kb = tl.key_tile(k) * KT;
+          if (wave < NB / 2) {                     // first read at the products of this tile
+            s_slot[(k + 3) & 7][tid] = slot_at(k + 3, entry);
+            entry = entry_at(k + 4);
+          }
+          const int last = kb + KT - 1;
+          uint64_t every = mapped[0];
+#pragma unroll
+          for (int i = 1; i < NB / 2; ++i) every &= mapped[i];
+          const bool all = every == ~0ull && last <= (kPrefix ? q.keys - 1 : tl.p_lo) &&
+                           (a.window == 0 || tl.p_hi - kb < a.window || last < a.sinks);
+          if (!all) {
+            // of the lane's keys, relative to kb + 4 g
+            const int hi = sight.hi - kb - 4 * g_, lo = sight.lo - kb - 4 * g_;
+            const int sk = sight.sinks - kb - 4 * g_;
+#pragma unroll
+            for (int t = 0; t < NB; ++t) {
+              const uint32_t there = (uint32_t)(mapped[t / 2] >> (32 * (t & 1))) >> (4 * g_);
+#pragma unroll
+              for (int v = 0; v < 16; ++v) {
+                const int b = 8 * (v / 4) + v % 4, j = 32 * t + b;
+                const bool is = (j <= hi) & ((j >= lo) | (j < sk)) & (((there >> b) & 1u) != 0u);
+                s[t][v] = is ? s[t][v] : FP8_NEG_INF;
+              }
             }
           }
-        }
-        if (careful && s_nan[cur] == serial) {     // NaN values: which ones does this row see?
+          float top = s[0][0];
+#pragma unroll
+          for (int t = 0; t < NB; ++t)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) top = __builtin_fmaxf(top, s[t][v]);
+          top = max_xor32(top) * c;
+          if (__ballot(top > m + 8.0f) != 0ull) {  // some row's maximum grew out of reach
+            const float m_new = __builtin_fmaxf(m, top);
+            const float alpha = __builtin_amdgcn_exp2f(m - base_of(m_new));
+            l *= alpha;
+#pragma unroll
+            for (int b = 0; b < OB; ++b)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[b][i] *= alpha;
+            m = m_new;
+          }
+          const float base = base_of(m);
+          float sum = 0.0f;
+          f16x8 p[KT / 16];
+#pragma unroll
+          for (int t = 0; t < NB; ++t)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+              const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][v], c, -base));
+              sum += e;
+              p[2 * t + v / 8][v % 8] = (_Float16)e;
+            }
+          l += sum;
+          // P is formed on this side of the barrier
+#pragma unroll
+          for (int i = 0; i < KT / 16; ++i) asm volatile("" : "+v"(p[i]));
+          asm volatile("" : "+v"(l));
+          __syncthreads();
+
+          if (careful && s_nan[cur] == k) {        // NaN values: which ones does this row see?
 #pragma unroll 1
-          for (int b = 0; b < KT; ++b) {
-            const int sb = s_slot[s0][b];
-            if (sb >= 0 && sight.sees(kb + b))
-              add_nans(nans, vc + (uint64_t)(uint32_t)sb * stride + g_ * (D / 2));
+            for (int b = 0; b < KT; ++b) {
+              const int sb = s_slot[k & 7][b];
+              if (sb >= 0 && sight.sees(kb + b))
+                add_nans(nans, vc + (uint64_t)(uint32_t)sb * stride + g_ * (D / 2));
+            }
           }
-        }
-        float top = s[0][0];
+          mend_v(k + 1, cur ^ 1);
+          // product e: V k with P k (k step e / OB, block e % OB), then K k + 1 with
+          // Q (k step e / NB, block e % NB); operands are read kAhead products ahead
+          constexpr int kPV = KT / 16 * OB, kProducts = kPV + KS * NB, kAhead = 5;
+          auto operand = [&](int e) {
+            if (e < kPV)
+              return *reinterpret_cast<const uint4*>(
+                  s_kv + (at_v ^ (32 * (e / OB)) ^ (64 * (e % OB & 1))) + (e % OB) * (64 * KT));
+            e -= kPV;
+            return *reinterpret_cast<const uint4*>(s_kv + (at_k ^ (32 * (e / NB))) +
+                                                   (e % NB) * (64 * D));
+          };
+          // what stands between them, kPer steps behind each product
+          constexpr int kSteps = kPutsK + kPutsV + kLoads;
+          constexpr int kPer = (kSteps + kProducts - 1) / kProducts;
+          const int slot = slot_k(k + 3);
+          const int4 slots = slots_v(k + 2);
+          const f32x16 zero = {};
+          uint4 f[kAhead + 1];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+          for (int e = 0; e < kAhead; ++e) f[e] = operand(e);
 #pragma unroll
-          for (int v = 0; v < 16; ++v) top = __builtin_fmaxf(top, s[t][v]);
-        top = max_xor32(top) * c;
-        if (__ballot(top > m + 8.0f) != 0ull) {    // some row's maximum grew out of reach
-          const float m_new = __builtin_fmaxf(m, top);
-          const float alpha = __builtin_amdgcn_exp2f(m - base_of(m_new));
-          l *= alpha;
+          for (int e = 0; e < kProducts; ++e) {
+            if (e + kAhead < kProducts) f[(e + kAhead) % (kAhead + 1)] = operand(e + kAhead);
+            const uint4 x = f[e % (kAhead + 1)];
+            if (e < kPV) {
+              o[e % OB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x),
+                                                                 p[e / OB], o[e % OB], 0, 0, 0);
+            } else {
+              const int i = (e - kPV) / NB, t = (e - kPV) % NB;
+              s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), qf[i],
+                                                             i == 0 ? zero : s[t], 0, 0, 0);
+            }
 #pragma unroll
-          for (int b = 0; b < OB; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[b][i] *= alpha;
-          m = m_new;
-        }
-        const float base = base_of(m);
-        float sum = 0.0f;
-        f16x8 p[4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][v], c, -base));
-            sum += e;
-            p[2 * t + v / 8][v % 8] = (_Float16)e;
+            for (int u = e * kPer; u < (e + 1) * kPer; ++u) {
+              if (u < kPutsK) put_k(u, put_at_k);
+              else if (u < kPutsK + kPutsV) put_v(u - kPutsK, put_at_v);
+              else if (u < kPutsK + kPutsV + KW / 4) fetch_k(u - kPutsK - kPutsV, slot);
+              else if (u < kSteps) fetch_v(u - kPutsK - kPutsV - KW / 4, slots);
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
-        l += sum;
-        {
-          const uint32_t at_v =
-              (2 + cur) * kBuf + n_ * 128 + ((g_ ^ n_ ^ (n_ >> 3)) & 7) * 16;
-#pragma unroll
-          for (int b = 0; b < OB; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                  *reinterpret_cast<const f16x8*>(s_kv + (at_v ^ (32 * i) ^ (64 * (b & 1))) +
-                                                  b * 4096),
-                  p[i], o[b], 0, 0, 0);
+          mapped_of(k + 1, true, mapped);
+          __syncthreads();
+          cur ^= 1;
         }
-        ++serial;
-        if (more) stage(cur ^ 1, s1, serial, gaps, t_);
-        if (wave == 0) s_slot[s2][lane] = slot_at(k + 2, entry);   // tile k - 1's place
-        __syncthreads();
-        cur ^= 1;
-        const int done = s0;
-        s0 = s1;
-        s1 = s2;
-        s2 = done;
+        if (!second) __syncthreads();
       }
       if (careful) break;
       bool bad = false;
@@ -1323,11 +1429,11 @@ int compute_units() {
   return n;
 }
 
-// Rows per request, on average, from which 128-row tiles are used.
+// Rows per request, on average, from which the large row tiles are used.
 bool many_rows(int64_t T, int64_t B, int64_t G) { return T * G > 32 * B; }
 
 struct Shape {
-  bool tiles;                   // 128-row tiles
+  bool tiles;                   // large row tiles
   int wgs, R;
 };
 
@@ -1335,8 +1441,8 @@ Shape shape_of(bool tiles, int D) {
   const int cus = compute_units();
   Shape s;
   s.tiles = tiles;
-  s.R = tiles ? kRowsT : kRowsD;
-  s.wgs = tiles ? (D == 256 ? cus : 2 * cus) : (D == 256 ? 2 * cus : 3 * cus);
+  s.R = tiles ? tile_waves(D) * 32 : kRowsD;
+  s.wgs = tiles ? cus : (D == 256 ? 2 * cus : 3 * cus);
   return s;
 }
 
@@ -1367,8 +1473,8 @@ template <int D, bool kPrefix, bool kJoin>
 void launch_main(const AttentionArgs& a, const Parts& p, const Shape& s, hipStream_t st) {
   const KernelArgs k = {a, p};
   if (s.tiles)
-    hipLaunchKernelGGL((attention_tile_kernel<D, kPrefix, kJoin>), dim3(s.wgs), dim3(kThreads), 0,
-                       st, k);
+    hipLaunchKernelGGL((attention_tile_kernel<D, kPrefix, kJoin>), dim3(s.wgs),
+                       dim3(tile_waves(D) * 64), 0, st, k);
   else
     hipLaunchKernelGGL((attention_rows_kernel<D, kPrefix, kJoin>), dim3(s.wgs), dim3(kThreads), 0,
                        st, k);
