@@ -362,8 +362,9 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-__device__ __forceinline__ uint32_t bf16_rne(float f) {
-  return f != f ? 0x7fc0u : f32_to_bf16_rne(f);
+// two fp32 to bf16, round to nearest even, in one instruction
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 __device__ __forceinline__ float max_xor32(float x) {
@@ -795,8 +796,8 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
       const int64_t flat = token * a.Hq + head;
       if (to.whole && !kJoin) {
         const float inv = ll == 0.0f ? 0.0f : fr->a.v_scale[0] / ll;
-        const uint32_t w0 = bf16_rne(acc[0] * inv) | (bf16_rne(acc[1] * inv) << 16);
-        const uint32_t w1 = bf16_rne(acc[2] * inv) | (bf16_rne(acc[3] * inv) << 16);
+        const uint32_t w0 = pack_bf16(acc[0] * inv, acc[1] * inv);
+        const uint32_t w1 = pack_bf16(acc[2] * inv, acc[3] * inv);
         *reinterpret_cast<uint2*>(fr->a.out + token * fr->a.ld_out + (int64_t)head * D + d) =
             make_uint2(w0, w1);
         if (fr->a.lse && d == 0) fr->a.lse[flat] = (base + __builtin_log2f(ll)) * kLn2;
@@ -951,11 +952,17 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
       uint32_t raw_k[KW], raw_v[4 * VW];
-      auto entry_at = [&](int k) {                 // a key per lane of the first waves
-        return k < kend ? entry_of(table, tl.key_tile(k) * KT + tid, q.keys, a.inv_page) : -1;
+      // The table's entry and the slot of key tid % KT of tile k.  The entry is
+      // read without a branch (of the last key where there is none), so that
+      // nothing waits for it before its use.
+      auto key_at = [&](int k) { return tl.key_tile(k) * KT + tid % KT; };
+      auto entry_at = [&](int k) {
+        const int j = key_at(k);
+        return table[div32((uint32_t)(j < q.keys ? j : q.keys - 1), a.inv_page)];
       };
       auto slot_at = [&](int k, int entry) {
-        return slot_of(entry, tl.key_tile(k) * KT + tid, a.page, a.inv_page, a.num_blocks);
+        const int j = key_at(k);
+        return slot_of((k < kend) & (j < q.keys) ? entry : -1, j, a.page, a.inv_page, a.num_blocks);
       };
       // Codes to registers: part i of a thread's piece of a key, and what it
       // takes of one of four keys' values.
@@ -985,22 +992,30 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
       auto slots_v = [&](int k) {
         return *reinterpret_cast<const int4*>(&s_slot[k & 7][first_v]);
       };
-      // Whether all keys of tile k are there; with the keys behind the last one
-      // counted as there, whether any is unmapped.
-      auto mapped_of = [&](int k, bool behind, uint64_t map[NB / 2]) {
+      // A key of tile k per lane (and 64 behind it): its slot
+      auto lane_slots = [&](int k, int x[NB / 2]) {
 #pragma unroll
-        for (int i = 0; i < NB / 2; ++i)
-          map[i] = __ballot((s_slot[k & 7][64 * i + lane] >= 0) |
-                            (behind & (tl.key_tile(k) * KT + 64 * i + lane >= q.keys)));
+        for (int i = 0; i < NB / 2; ++i) x[i] = s_slot[k & 7][64 * i + lane];
+      };
+      // Whether a key of tile k is not there; whether one before the last key is
+      // not, that is, in an unmapped page.
+      auto any_gap = [&](const int x[NB / 2]) {
+        bool gap = x[0] < 0;
+#pragma unroll
+        for (int i = 1; i < NB / 2; ++i) gap |= x[i] < 0;
+        return __ballot(gap) != 0ull;
+      };
+      auto any_hole = [&](int k, const int x[NB / 2]) {
+        const int j = tl.key_tile(k) * KT + lane;
+        bool hole = (x[0] < 0) & (j < q.keys);
+#pragma unroll
+        for (int i = 1; i < NB / 2; ++i) hole |= (x[i] < 0) & (j + 64 * i < q.keys);
+        return __ballot(hole) != 0ull;
       };
       // Rare: values of keys that are not there become zeros, whatever the
       // address held, and a careful pass takes the NaNs out.
-      auto mend_v = [&](int k, int buf) {
-        uint64_t there[NB / 2], every = ~0ull;
-        mapped_of(k, false, there);
-#pragma unroll
-        for (int i = 0; i < NB / 2; ++i) every &= there[i];
-        if (every != ~0ull) {
+      auto mend_v = [&](int k, int buf, bool gap) {
+        if (gap) {
           const int4 sv = slots_v(k);
           const int s4[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
@@ -1057,34 +1072,60 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
       };
       if (at.k < kend) {
         if (tid < 2) s_nan[tid] = -1;
-        int entry = -1;                            // of tile k + 3
-        if (wave < NB / 2) {
+        int entry;                                 // of tile k + 4
+        {
+          int first[4];
 #pragma unroll
-          for (int i = 0; i < 3; ++i)
-            s_slot[(at.k + i) & 7][tid] = slot_at(at.k + i, entry_at(at.k + i));
-          entry = entry_at(at.k + 3);
+          for (int i = 0; i < 4; ++i) first[i] = entry_at(at.k + i);
+          entry = entry_at(at.k + 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            s_slot[(at.k + i) & 7][tid % KT] = slot_at(at.k + i, first[i]);
         }
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 3; ++j) {              // K j to LDS, then K j + 1; V j - 1, V j
-          if (j > 0) {
-#pragma unroll
-            for (int u = 0; u < kPutsK; ++u) put_k(u, to_k + (j - 1) * kBuf);
-          }
-          const int slot = slot_k(at.k + j);
+        // K k, K k + 1 and V k to LDS; K k + 2 and V k + 1 stay in registers
+        int x[NB / 2];
+        lane_slots(at.k, x);
+        uint32_t k0[KW], v0[4 * VW], k1[KW];
+        const auto load_k = [&](int k) {
+          const int slot = slot_k(k);
 #pragma unroll
           for (int i = 0; i < KW / 4; ++i) fetch_k(i, slot);
-          if (j < 2) {
-            if (j == 1) {
-              mend_v(at.k, 0);
+        };
+        const auto load_v = [&](int k) {
+          const int4 slots = slots_v(k);
 #pragma unroll
-              for (int u = 0; u < kPutsV; ++u) put_v(u, to_v);
-            }
-            const int4 slots = slots_v(at.k + j);
+          for (int e = 0; e < 4; ++e) fetch_v(e, slots);
+        };
+        load_k(at.k);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) fetch_v(e, slots);
-          }
-        }
+        for (int i = 0; i < KW; ++i) k0[i] = raw_k[i];
+        load_v(at.k);
+#pragma unroll
+        for (int i = 0; i < 4 * VW; ++i) v0[i] = raw_v[i];
+        load_k(at.k + 1);
+#pragma unroll
+        for (int i = 0; i < KW; ++i) k1[i] = raw_k[i];
+        load_k(at.k + 2);
+        load_v(at.k + 1);
+        uint32_t k2[KW], v1[4 * VW];
+#pragma unroll
+        for (int i = 0; i < KW; ++i) k2[i] = raw_k[i], raw_k[i] = k0[i];
+#pragma unroll
+        for (int i = 0; i < 4 * VW; ++i) v1[i] = raw_v[i], raw_v[i] = v0[i];
+#pragma unroll
+        for (int u = 0; u < kPutsK; ++u) put_k(u, to_k);
+        mend_v(at.k, 0, any_gap(x));
+#pragma unroll
+        for (int u = 0; u < kPutsV; ++u) put_v(u, to_v);
+#pragma unroll
+        for (int i = 0; i < KW; ++i) raw_k[i] = k1[i];
+#pragma unroll
+        for (int u = 0; u < kPutsK; ++u) put_k(u, to_k + kBuf);
+#pragma unroll
+        for (int i = 0; i < KW; ++i) raw_k[i] = k2[i];
+#pragma unroll
+        for (int i = 0; i < 4 * VW; ++i) raw_v[i] = v1[i];
         __syncthreads();
         if (second) __syncthreads();               // half a period behind
         // S^T: block t holds keys 32 t + 8 (v / 4) + 4 g + v % 4 of row n
@@ -1102,8 +1143,11 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
                 qf[i], s[t], 0, 0, 0);
         __syncthreads();
         int cur = 0;
-        uint64_t mapped[NB / 2];
-        mapped_of(at.k, true, mapped);
+        // tile k has unmapped keys; V k + 1 lacks some
+        int x0[NB / 2], x1[NB / 2];
+        lane_slots(at.k, x0);
+        lane_slots(at.k + 1, x1);
+        bool holes = any_hole(at.k, x0), gap = any_gap(x1);
 #pragma unroll 1
         for (int k = at.k; k < kend; ++k) {
           // what is formed from these is formed in each pass: kept through the
@@ -1116,28 +1160,51 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
           put_at_k += cur * kBuf;
           put_at_v += (cur ^ 1) * kBuf;
           const int kb = tl.key_tile(k) * KT;
-          if (wave < NB / 2) {                     // first read at the products of this tile
-            s_slot[(k + 3) & 7][tid] = slot_at(k + 3, entry);
-            entry = entry_at(k + 4);
-          }
           const int last = kb + KT - 1;
-          uint64_t every = mapped[0];
+          // three kinds of keys that not every row sees, each rare: behind the
+          // row (or the last key), before its window, in an unmapped page
+          if (last > (kPrefix ? q.keys - 1 : tl.p_lo) || last >= q.keys) {
+            const int hi = sight.hi - kb - 4 * g_;
 #pragma unroll
-          for (int i = 1; i < NB / 2; ++i) every &= mapped[i];
-          const bool all = every == ~0ull && last <= (kPrefix ? q.keys - 1 : tl.p_lo) &&
-                           (a.window == 0 || tl.p_hi - kb < a.window || last < a.sinks);
-          if (!all) {
-            // of the lane's keys, relative to kb + 4 g
-            const int hi = sight.hi - kb - 4 * g_, lo = sight.lo - kb - 4 * g_;
-            const int sk = sight.sinks - kb - 4 * g_;
-#pragma unroll
-            for (int t = 0; t < NB; ++t) {
-              const uint32_t there = (uint32_t)(mapped[t / 2] >> (32 * (t & 1))) >> (4 * g_);
+            for (int t = 0; t < NB; ++t)
 #pragma unroll
               for (int v = 0; v < 16; ++v) {
-                const int b = 8 * (v / 4) + v % 4, j = 32 * t + b;
-                const bool is = (j <= hi) & ((j >= lo) | (j < sk)) & (((there >> b) & 1u) != 0u);
-                s[t][v] = is ? s[t][v] : FP8_NEG_INF;
+                s[t][v] = 32 * t + 8 * (v / 4) + v % 4 <= hi ? s[t][v] : FP8_NEG_INF;
+                if (v % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // few masks at a time
+              }
+          }
+          if (!kPrefix && a.window > 0 && tl.p_hi - kb >= a.window && last >= a.sinks) {
+            const int lo = sight.lo - kb - 4 * g_, sk = sight.sinks - kb - 4 * g_;
+            if (kb >= a.sinks) {
+#pragma unroll
+              for (int t = 0; t < NB; ++t)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                  s[t][v] = 32 * t + 8 * (v / 4) + v % 4 >= lo ? s[t][v] : FP8_NEG_INF;
+                  if (v % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+              int lo2 = lo;
+              asm volatile("" : "+v"(lo2));        // its comparisons are its own
+#pragma unroll
+              for (int t = 0; t < NB; ++t)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                  const int j = 32 * t + 8 * (v / 4) + v % 4;
+                  s[t][v] = (j >= lo2) | (j < sk) ? s[t][v] : FP8_NEG_INF;
+                  if (v % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+          }
+          if (holes) {
+#pragma unroll
+            for (int t = 0; t < NB; ++t) {
+              const uint64_t map = __ballot(s_slot[k & 7][64 * (t / 2) + lane] >= 0);
+              const uint32_t there = (uint32_t)(map >> (32 * (t & 1))) >> (4 * g_);
+#pragma unroll
+              for (int v = 0; v < 16; ++v) {
+                s[t][v] = (there >> (8 * (v / 4) + v % 4)) & 1u ? s[t][v] : FP8_NEG_INF;
+                if (v % 4 == 3) __builtin_amdgcn_sched_barrier(0);
               }
             }
           }
@@ -1183,7 +1250,8 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
                 add_nans(nans, vc + (uint64_t)(uint32_t)sb * stride + g_ * (D / 2));
             }
           }
-          mend_v(k + 1, cur ^ 1);
+          __builtin_amdgcn_s_setprio(2);           // the products go first
+          mend_v(k + 1, cur ^ 1, gap);
           // product e: V k with P k (k step e / OB, block e % OB), then K k + 1 with
           // Q (k step e / NB, block e % NB); operands are read kAhead products ahead
           constexpr int kPV = KT / 16 * OB, kProducts = kPV + KS * NB, kAhead = 5;
@@ -1200,6 +1268,12 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
           constexpr int kPer = (kSteps + kProducts - 1) / kProducts;
           const int slot = slot_k(k + 3);
           const int4 slots = slots_v(k + 2);
+          lane_slots(k + 1, x0);
+          lane_slots(k + 2, x1);
+          // slots of tile k + 4, which every pair of waves writes alike and which
+          // the products of tile k + 1 read; the entries behind them
+          s_slot[(k + 4) & 7][tid % KT] = slot_at(k + 4, entry);
+          entry = entry_at(k + 5);
           const f32x16 zero = {};
           uint4 f[kAhead + 1];
 #pragma unroll
@@ -1225,7 +1299,9 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
             }
             __builtin_amdgcn_sched_barrier(0);
           }
-          mapped_of(k + 1, true, mapped);
+          holes = any_hole(k + 1, x0);
+          gap = any_gap(x1);
+          __builtin_amdgcn_s_setprio(0);
           __syncthreads();
           cur ^= 1;
         }
@@ -1270,7 +1346,7 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              w[e] = bf16_rne(o[b][i + 2 * e] * inv) | (bf16_rne(o[b][i + 2 * e + 1] * inv) << 16);
+              w[e] = pack_bf16(o[b][i + 2 * e] * inv, o[b][i + 2 * e + 1] * inv);
             *reinterpret_cast<uint4*>(po + 16 * b + i) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         if (fr->a.lse && g == 0) fr->a.lse[flat] = (base_of(m) + __builtin_log2f(l)) * kLn2;
@@ -1352,7 +1428,11 @@ __device__ __forceinline__ void write_row(const AttentionArgs& a, const Sum<D>& 
   const float inv = s.l == 0.0f ? 0.0f : a.v_scale[0] / s.l;
   uint16_t* p = a.out + token * a.ld_out + (int64_t)head * D + lane * (D / 64);
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) p[i] = (uint16_t)bf16_rne(s.o[i] * inv);
+  for (int i = 0; i < D / 64; i += 2) {
+    const uint32_t w = pack_bf16(s.o[i] * inv, s.o[i + 1 < D / 64 ? i + 1 : i] * inv);
+    if (D == 64) p[0] = (uint16_t)w;
+    else *reinterpret_cast<uint32_t*>(p + i) = w;
+  }
   if (a.lse && lane == 0) a.lse[token * a.Hq + head] = (base + __builtin_log2f(s.l)) * kLn2;
 }
 
