@@ -44,6 +44,8 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -242,7 +244,7 @@ struct Place {
 };
 
 // Finds this workgroup's share and where it begins.
-template <bool kPrefix, int R, int KT, int kWaves>
+template <bool kPrefix, int R, int KT, int kWaves, int kLeast>
 __device__ __forceinline__ Place find_share(const AttentionArgs& a, int wg, int wgs,
                                             int64_t* s_wave, int64_t* s_found) {
   constexpr int kThreads = kWaves * 64;
@@ -263,7 +265,8 @@ __device__ __forceinline__ Place find_share(const AttentionArgs& a, int wg, int 
     total += all;
   }
   p.share = div64(total + wgs - 1, 1.0 / (double)wgs);
-  p.inv_share = 1.0 / (double)(p.share > 0 ? p.share : 1);
+  p.share = p.share > kLeast ? p.share : kLeast;
+  p.inv_share = 1.0 / (double)p.share;
   p.pos = p.share * wg;
   p.end = p.pos + p.share < total ? p.pos + p.share : total;
   p.r = p.m = p.h = p.k = 0;
@@ -524,39 +527,46 @@ constexpr int kKeysD = 128;
 
 template <int D>
 struct Unit {
-  uint32_t k[2][D / 16];   // lane (n, g): D/4 bytes at g D/4 of keys n and 16 + n
+  uint32_t k[2][D / 16];   // lane (n, g): 16 bytes at 64 i + 16 g of keys n and 16 + n
   uint32_t v[8][D / 64];   // lane (n, g): D/16 bytes at n D/16 of keys 4g+i, 16+4g+i
 };
 
-template <int D>
+// kc, vc: this lane's bytes of slot 0.  kQuads: blocks of a multiple of 4
+// tokens, so that keys 4 i .. 4 i + 3 lie behind one another.
+template <int D, bool kQuads>
 __device__ __forceinline__ void load_unit(Unit<D>& u, const uint8_t* kc, const uint8_t* vc,
                                           uint32_t stride, int slot) {
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int s = __shfl(slot, 16 * t + n);
-    const uint8_t* p = kc + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride + g * (D / 4);
+    const uint8_t* p = kc + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4*>(p + 16 * i);
+      const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 64 * i));
       u.k[t][4 * i] = x.x;
       u.k[t][4 * i + 1] = x.y;
       u.k[t][4 * i + 2] = x.z;
       u.k[t][4 * i + 3] = x.w;
     }
   }
+  const uint8_t* p = nullptr;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int s = __shfl(slot, (e < 4 ? 0 : 12) + 4 * g + e);
-    const uint8_t* p = vc + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride + n * (D / 16);
+    if (kQuads && e % 4 != 0) {
+      p += stride;
+    } else {
+      const int s = __shfl(slot, (e < 4 ? 0 : 12) + 4 * g + e);
+      p = vc + (uint64_t)(uint32_t)(s < 0 ? 0 : s) * stride;
+    }
     if constexpr (D == 64) {
-      u.v[e][0] = *reinterpret_cast<const uint32_t*>(p);
+      u.v[e][0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
     } else if constexpr (D == 128) {
-      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
       u.v[e][0] = x.x;
       u.v[e][1] = x.y;
     } else {
-      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
       u.v[e][0] = x.x;
       u.v[e][1] = x.y;
       u.v[e][2] = x.z;
@@ -574,8 +584,9 @@ __device__ __forceinline__ void v_operands(const uint32_t w[8], f16x8 out[4]) {
   for (int b = 0; b < 4; ++b) out[b] = f16_of_codes(lo[b], hi[b]);
 }
 
-template <int D, bool kPrefix, bool kJoin>
-__global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs args) {
+template <int D, bool kPrefix, bool kJoin, bool kQuads>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_kernel(
+    KernelArgs args) {
   constexpr int R = kRowsD, KT = kKeysD, OT = D / 16;
   constexpr int kPitch = D + 4;                    // floats: rows start in other banks
   constexpr int kNanWords = D >= 128 ? D / 128 : 1;   // of a lane's D / 4 values
@@ -586,7 +597,7 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int wg = blockIdx.x;
-  Place at = find_share<kPrefix, R, KT, 4>(a, wg, gridDim.x, s_wave, s_found);
+  Place at = find_share<kPrefix, R, KT, 4, 2>(a, wg, gridDim.x, s_wave, s_found);
   if (!kJoin && tid == 0) args.parts.split[wg].parts = 0;
   const uint32_t stride = (uint32_t)a.Hk * D;
   const Factor fac = factor_of(a);
@@ -616,9 +627,10 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
     for (int i = 0; i < D / 32; ++i) qf[i] = bf16x8{};
     if (n < rows) {
       const uint16_t* p = a.q + (int64_t)(q.token0 + i_n) * a.ld_q +
-                          (int64_t)(at.h * a.G + row0 + n - i_n * a.G) * D + g * (D / 4);
+                          (int64_t)(at.h * a.G + row0 + n - i_n * a.G) * D + g * 16;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) qf[i] = load_query(p + 8 * i, fac.flip);
+      for (int i = 0; i < D / 32; ++i)
+        qf[i] = load_query(p + 64 * (i / 2) + 8 * (i % 2), fac.flip);
     }
     float m = FP8_NEG_INF, l = 0.0f;
     f32x4 o[OT];
@@ -630,28 +642,31 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
     const int kend = k1 < count ? k1 : count;      // an item of no keys has no tile
     if (at.k < kend) {
       const int32_t* table = kPrefix ? a.prefix_table : a.table + (int64_t)at.r * a.ld_table;
-      const uint8_t* kc = a.kc + (int64_t)at.h * D;
-      const uint8_t* vc = a.vc + (int64_t)at.h * D;
+      const uint8_t* kc = a.kc + (int64_t)at.h * D + g * 16;
+      const uint8_t* vc = a.vc + (int64_t)at.h * D + n * (D / 16);
       auto key_at = [&](int k) { return tl.key_tile(k) * KT + wave * 32 + (lane & 31); };
+      // read without a branch (the last key's where there is none), so that
+      // nothing waits for it before its use
       auto entry_at = [&](int k) {
-        return k < kend ? entry_of(table, key_at(k), q.keys, a.inv_page) : -1;
+        const int j = key_at(k);
+        return table[div32((uint32_t)(j < q.keys ? j : q.keys - 1), a.inv_page)];
       };
       auto slot_at = [&](int k, int entry) {
-        return slot_of(entry, key_at(k), a.page, a.inv_page, a.num_blocks);
+        const int j = key_at(k);
+        return slot_of(k < kend && j < q.keys ? entry : -1, j, a.page, a.inv_page, a.num_blocks);
       };
-      Unit<D> next;
+      // while a unit is computed the next one's codes are in flight
+      Unit<D> unit[2];
       int slot = slot_at(at.k, entry_at(at.k)), entry = entry_at(at.k + 1);
-      load_unit<D>(next, kc, vc, stride, slot);
-#pragma unroll 1
-      for (int k = at.k; k < kend; ++k) {
-        Unit<D> now = next;
+      load_unit<D, kQuads>(unit[0], kc, vc, stride, slot);
+      auto step = [&](int k, Unit<D>& now, Unit<D>& next) {
         const int kb = tl.key_tile(k) * KT + wave * 32;
         const int mine = slot;
         slot = slot_at(k + 1, entry);
         entry = entry_at(k + 2);
-        if (k + 1 < kend) load_unit<D>(next, kc, vc, stride, slot);
+        load_unit<D, kQuads>(next, kc, vc, stride, slot);
         const uint32_t mapped = (uint32_t)__ballot(mine >= 0);
-        if (mapped == 0u) continue;                // nothing of these 32 keys is there
+        if (mapped == 0u) return;                  // nothing of these 32 keys is there
         // S^T: keys 16 t + 4 g + i of row n
         f32x4 s[2];
 #pragma unroll
@@ -696,7 +711,8 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
             for (int b = 0; b < 32; ++b) {
               const int sb = __shfl(mine, b);
               if (sb >= 0 && sight.sees(kb + b)) {
-                const uint8_t* p = vc + (uint64_t)(uint32_t)sb * stride + g * (D / 4);
+                const uint8_t* p = a.vc + (int64_t)at.h * D + (uint64_t)(uint32_t)sb * stride +
+                                   g * (D / 4);
                 if constexpr (D >= 128) {
                   add_nans(nans, p);
                 } else {                           // 16 values of a lane
@@ -714,10 +730,17 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, s[t][i]);
         top = max_xor32(max_xor16(top)) * c;
-        const float m_new = __builtin_fmaxf(m, top);
-        const float base = base_of(m_new);
-        const float alpha = __builtin_amdgcn_exp2f(m - base);
-        m = m_new;
+        // the base moves where a row's maximum passes it by 2^8 (see the larger
+        // tiles below)
+        if (__ballot(top > m + 8.0f) != 0ull) {
+          const float m_new = __builtin_fmaxf(m, top);
+          const float alpha = __builtin_amdgcn_exp2f(m - base_of(m_new));
+          l *= alpha;
+#pragma unroll
+          for (int j = 0; j < OT; ++j) o[j] *= alpha;
+          m = m_new;
+        }
+        const float base = base_of(m);
         float sum = 0.0f;
         f16x8 p;
 #pragma unroll
@@ -728,9 +751,7 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
             sum += e;
             p[4 * t + i] = (_Float16)e;
           }
-        l = __builtin_fmaf(l, alpha, sum);
-#pragma unroll
-        for (int j = 0; j < OT; ++j) o[j] *= alpha;
+        l += sum;
 #pragma unroll
         for (int w = 0; w < D / 64; ++w) {
           uint32_t col[8];
@@ -742,6 +763,13 @@ __global__ __launch_bounds__(kThreads) void attention_rows_kernel(KernelArgs arg
           for (int b = 0; b < 4; ++b)
             o[4 * w + b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vo[b], p, o[4 * w + b], 0, 0, 0);
         }
+      };
+#pragma unroll 1
+      for (int k = at.k;;) {
+        step(k, unit[0], unit[1]);
+        if (++k >= kend) break;
+        step(k, unit[1], unit[0]);
+        if (++k >= kend) break;
       }
     }
     l = sum_xor32(sum_xor16(l));
@@ -877,7 +905,7 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
   const int wgs = gridDim.x;
   const int wg = wgs % 8 == 0 ? (int)(blockIdx.x % 8) * (wgs / 8) + (int)(blockIdx.x / 8)
                               : (int)blockIdx.x;
-  Place at = find_share<kPrefix, R, KT, kWaves>(a, wg, wgs, s_wave, s_found);
+  Place at = find_share<kPrefix, R, KT, kWaves, 1>(a, wg, wgs, s_wave, s_found);
   if (!kJoin && tid == 0) args.parts.split[wg].parts = 0;
   const uint32_t stride = (uint32_t)a.Hk * D;
   const Factor fac = factor_of(a);
@@ -1254,7 +1282,7 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
           mend_v(k + 1, cur ^ 1, gap);
           // product e: V k with P k (k step e / OB, block e % OB), then K k + 1 with
           // Q (k step e / NB, block e % NB); operands are read kAhead products ahead
-          constexpr int kPV = KT / 16 * OB, kProducts = kPV + KS * NB, kAhead = 5;
+          constexpr int kPV = KT / 16 * OB, kProducts = kPV + KS * NB, kAhead = 4;
           auto operand = [&](int e) {
             if (e < kPV)
               return *reinterpret_cast<const uint4*>(
@@ -1410,15 +1438,31 @@ __device__ __forceinline__ void add_row(Sum<D>& s, const float* ml, const float*
     s.o[i] = __builtin_fmaf(o[row * D + lane * (D / 64) + i], f, s.o[i]);
 }
 
-template <int D>
+// kTogether: parts whose loads go out together
+template <int D, int kTogether>
 __device__ __forceinline__ void add_parts(Sum<D>& s, const float* ml, const float* o, int64_t f,
                                           int np, int R, float base, int j0, int step) {
-  int j = j0;
-  for (; j + 3 * step < np; j += 4 * step) {       // four parts' loads together
+  for (int j = j0; j < np; j += kTogether * step) {
+    float f_[kTogether], l_[kTogether], o_[kTogether][D / 64];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) add_row<D>(s, ml, o, part_row(f, j + u * step, R), base);
+    for (int u = 0; u < kTogether; ++u) {
+      const bool is = j + u * step < np;
+      const int64_t row = part_row(f, is ? j + u * step : j, R);
+      f_[u] = is ? ml[row * 2] : FP8_NEG_INF;
+      l_[u] = ml[row * 2 + 1];
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        o_[u][i] = o[row * D + (threadIdx.x & 63) * (D / 64) + i];
+    }
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u) {
+      const float w = __builtin_amdgcn_exp2f(f_[u] - base);
+      if (j + u * step >= np) break;
+      s.l = __builtin_fmaf(l_[u], w, s.l);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) s.o[i] = __builtin_fmaf(o_[u][i], w, s.o[i]);
+    }
   }
-  for (; j < np; j += step) add_row<D>(s, ml, o, part_row(f, j, R), base);
 }
 
 template <int D>
@@ -1453,7 +1497,10 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
     const int64_t f = ((int64_t)2 * blockIdx.x + 1) * R + row;
     const float base = base_of(parts_max(parts.ml, f, sp.parts, R));
     Sum<D> s = {};
-    add_parts<D>(s, parts.ml, parts.o, f, sp.parts, R, base, wide ? wave : 0, wide ? 4 : 1);
+    if (wide)
+      add_parts<D, 8>(s, parts.ml, parts.o, f, sp.parts, R, base, wave, 4);
+    else
+      add_parts<D, 2>(s, parts.ml, parts.o, f, sp.parts, R, base, 0, 1);
     if (wide) {
       __syncthreads();
       if (lane == 0) s_l[wave] = s.l;
@@ -1486,9 +1533,9 @@ __global__ __launch_bounds__(kThreads) void attention_prefix_join_kernel(Attenti
   const float m2 = w2.y ? parts_max(p2.ml, w2.x, w2.y, R2) : p2.whole_ml[flat * 2];
   const float base = base_of(__builtin_fmaxf(m1, m2));
   Sum<D> s = {};
-  if (w1.y) add_parts<D>(s, p1.ml, p1.o, w1.x, w1.y, R1, base, 0, 1);
+  if (w1.y) add_parts<D, 8>(s, p1.ml, p1.o, w1.x, w1.y, R1, base, 0, 1);
   else add_row<D>(s, p1.whole_ml, p1.whole_o, flat, base);
-  if (w2.y) add_parts<D>(s, p2.ml, p2.o, w2.x, w2.y, R2, base, 0, 1);
+  if (w2.y) add_parts<D, 2>(s, p2.ml, p2.o, w2.x, w2.y, R2, base, 0, 1);
   else add_row<D>(s, p2.whole_ml, p2.whole_o, flat, base);
   const int64_t token = flat / a.Hq;
   write_row<D>(a, s, base, token, (int)(flat - token * a.Hq));
@@ -1522,7 +1569,7 @@ Shape shape_of(bool tiles, int D) {
   Shape s;
   s.tiles = tiles;
   s.R = tiles ? tile_waves(D) * 32 : kRowsD;
-  s.wgs = tiles ? cus : (D == 256 ? 2 * cus : 3 * cus);
+  s.wgs = tiles ? cus : (D == 256 ? cus : 2 * cus);
   return s;
 }
 
@@ -1555,9 +1602,12 @@ void launch_main(const AttentionArgs& a, const Parts& p, const Shape& s, hipStre
   if (s.tiles)
     hipLaunchKernelGGL((attention_tile_kernel<D, kPrefix, kJoin>), dim3(s.wgs),
                        dim3(tile_waves(D) * 64), 0, st, k);
+  else if (a.page % 4 == 0)
+    hipLaunchKernelGGL((attention_rows_kernel<D, kPrefix, kJoin, true>), dim3(s.wgs),
+                       dim3(kThreads), 0, st, k);
   else
-    hipLaunchKernelGGL((attention_rows_kernel<D, kPrefix, kJoin>), dim3(s.wgs), dim3(kThreads), 0,
-                       st, k);
+    hipLaunchKernelGGL((attention_rows_kernel<D, kPrefix, kJoin, false>), dim3(s.wgs),
+                       dim3(kThreads), 0, st, k);
 }
 
 template <int D>
