@@ -177,7 +177,44 @@ constexpr int kThreads = 256;     // of the 16-row and the joining kernels
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-__device__ __forceinline__ int64_t wave_scan(int64_t x) {   // inclusive
+__device__ __forceinline__ int64_t lane_of(int64_t x, int lane) {   // uniform lane
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)x >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t add_dpp(uint32_t x) {
+  return x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kCtrl, kRows, 0xf, false);
+}
+
+// values that all lanes hold alike, to scalar registers
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)x);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)x >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ Request uniform_request(Request q) {
+  q.token0 = uniform(q.token0);
+  q.n = uniform(q.n);
+  q.p0 = uniform(q.p0);
+  q.keys = uniform(q.keys);
+  return q;
+}
+
+// Inclusive sums over the wave's lanes of x >= 0: within rows of 16 lanes, then
+// across them, in 32 bits where no sum can pass them.
+__device__ __forceinline__ int64_t wave_scan(int64_t x) {
+  if (__ballot(x >= (1ll << 25)) == 0ull) {
+    uint32_t v = (uint32_t)x;
+    v = add_dpp<0x111, 0xf>(v);                    // row_shr:1, 2, 4, 8
+    v = add_dpp<0x112, 0xf>(v);
+    v = add_dpp<0x114, 0xf>(v);
+    v = add_dpp<0x118, 0xf>(v);
+    v = add_dpp<0x142, 0xa>(v);                    // row_bcast:15 into rows 1 and 3
+    v = add_dpp<0x143, 0xc>(v);                    // row_bcast:31 into rows 2 and 3
+    return v;
+  }
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -205,115 +242,135 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_wave, int64_
   return before + x - v;
 }
 
-// Tiles of all row tiles of request r (0 behind the last), one request per
-// lane.  A lane sums up to 4 row tiles itself; longer requests are taken one by
-// one by the whole wave.
-template <bool kPrefix, int R, int KT>
-__device__ __forceinline__ int64_t request_cost(const AttentionArgs& a, int r, int B) {
-  Request q = {};
-  if (r < B) q = load_request<kPrefix>(a, r);
-  const int mt = r < B ? row_tiles(a, q, R) : 0;
+// Tiles of all row tiles of a request of mt, one request per lane.  A lane sums
+// up to 4 row tiles itself; longer requests are taken one by one by the whole
+// wave.
+template <int R, int KT>
+__device__ __forceinline__ int64_t request_cost(const AttentionArgs& a, const Request& q, int mt) {
   int64_t c = 0;
-  if (kPrefix) {
-    if (mt > 0) c = (int64_t)mt * cost_of(tiles_of<kPrefix, R, KT>(a, q, 0));
-    return c * a.Hk;
-  }
   if (mt <= 4)
-    for (int m = 0; m < mt; ++m) c += cost_of(tiles_of<kPrefix, R, KT>(a, q, m));
+    for (int m = 0; m < mt; ++m) c += cost_of(tiles_of<false, R, KT>(a, q, m));
   for (uint64_t rest = __ballot(mt > 4); rest != 0ull; rest &= rest - 1) {
-    const int of = __ffsll((unsigned long long)rest) - 1;
+    const int of = __ffsll((unsigned long long)rest) - 1, lane = threadIdx.x & 63;
     Request x;
     x.token0 = 0;
-    x.n = uniform(__shfl(q.n, of));
-    x.p0 = uniform(__shfl(q.p0, of));
-    x.keys = uniform(__shfl(q.keys, of));
-    const int xt = uniform(__shfl(mt, of)), lane = threadIdx.x & 63;
+    x.n = __builtin_amdgcn_readlane(q.n, of);
+    x.p0 = __builtin_amdgcn_readlane(q.p0, of);
+    x.keys = __builtin_amdgcn_readlane(q.keys, of);
+    const int xt = __builtin_amdgcn_readlane(mt, of);
     int64_t part = 0;
-    for (int m = lane; m < xt; m += 64) part += cost_of(tiles_of<kPrefix, R, KT>(a, x, m));
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) part += __shfl_xor(part, d);
+    for (int m = lane; m < xt; m += 64) part += cost_of(tiles_of<false, R, KT>(a, x, m));
+    part = lane_of(wave_scan(part), 63);
     if (lane == of) c = part;
   }
-  return c * a.Hk;
+  return c;
 }
 
 struct Place {
   int64_t share, pos, end;   // tiles per workgroup, this one's range
   double inv_share;
   int r, m, h, k;            // where pos is
+  Request q;                 // request r
 };
 
-// Finds this workgroup's share and where it begins.
+// Finds this workgroup's share of all tiles (those of the KV heads together)
+// and where it begins.
 template <bool kPrefix, int R, int KT, int kWaves, int kLeast>
 __device__ __forceinline__ Place find_share(const AttentionArgs& a, int wg, int wgs,
                                             int64_t* s_wave, int64_t* s_found) {
   constexpr int kThreads = kWaves * 64;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63;
   const int B = kPrefix ? 1 : a.B;
+  const auto cost_at = [&](int r, Request& q) -> int64_t {   // per KV head
+    q = {};
+    if (r >= B) q.n = 0;
+    else q = load_request<kPrefix>(a, r);
+    const int mt = row_tiles(a, q, R);
+    if (kPrefix) return mt > 0 ? (int64_t)mt * cost_of(tiles_of<true, R, KT>(a, q, 0)) : 0;
+    return request_cost<R, KT>(a, q, mt);
+  };
   Place p;
-  int64_t total = 0;
-  // with at most one request per thread the first pass's scan is kept
-  int64_t first_cost = 0, first_before = 0;
-  for (int r0 = 0; r0 < B; r0 += kThreads) {
-    const int64_t c = request_cost<kPrefix, R, KT>(a, r0 + tid, B);
-    int64_t all;
-    const int64_t before = block_scan<kWaves>(c, s_wave, all);
-    if (r0 == 0) {
-      first_cost = c;
-      first_before = before;
+  p.r = p.m = p.h = p.k = 0;
+  Request q;
+  int64_t c = 0, upto = 0, total = 0;              // of this lane's request; of all
+  const bool one_wave = B <= 64;                   // every wave takes all requests
+  if (kPrefix) {
+    total = cost_at(0, q);
+  } else if (one_wave) {
+    c = cost_at(lane, q);
+    upto = wave_scan(c);
+    total = lane_of(upto, 63);
+  } else {
+    for (int r0 = 0; r0 < B; r0 += kThreads) {
+      int64_t all;
+      block_scan<kWaves>(cost_at(r0 + tid, q), s_wave, all);
+      total += all;
     }
-    total += all;
   }
-  p.share = div64(total + wgs - 1, 1.0 / (double)wgs);
+  total *= a.Hk;
+  total = uniform64(total);
+  p.share = uniform64(div64(total + wgs - 1, 1.0 / (double)wgs));
   p.share = p.share > kLeast ? p.share : kLeast;
-  p.inv_share = 1.0 / (double)p.share;
+  p.inv_share = __builtin_bit_cast(
+      double, uniform64(__builtin_bit_cast(int64_t, 1.0 / (double)p.share)));
   p.pos = p.share * wg;
   p.end = p.pos + p.share < total ? p.pos + p.share : total;
-  p.r = p.m = p.h = p.k = 0;
+  p.q = uniform_request(q);
   if (p.pos >= p.end) return p;
-  int64_t base = 0;
-  for (int r0 = 0; r0 < B; r0 += kThreads) {
-    int64_t c = first_cost, before = first_before, all = total;
-    if (B > kThreads) {
-      c = request_cost<kPrefix, R, KT>(a, r0 + tid, B);
-      before = block_scan<kWaves>(c, s_wave, all);
-    }
-    const int64_t x = p.pos - base - before;
-    if (x >= 0 && x < c) {          // one thread of one pass
-      s_found[0] = r0 + tid;
-      s_found[1] = x;
-    }
-    base += all;
-    if (p.pos < base) break;        // uniform
-  }
-  __syncthreads();
-  p.r = uniform((int)s_found[0]);
-  int64_t x = s_found[1];
-  const Request q = load_request<kPrefix>(a, p.r);
-  int64_t c = 1;
   if (kPrefix) {
-    c = cost_of(tiles_of<kPrefix, R, KT>(a, q, 0));
-    p.m = uniform((int)div64(x, 1.0 / (double)(c * a.Hk)));
-    x -= (int64_t)p.m * c * a.Hk;
-  } else {
-    const int mt = row_tiles(a, q, R), lane = tid & 63;
-    for (int m0 = 0; m0 < mt; m0 += 64) {           // every wave alike
-      const int m = m0 + lane;
-      const int64_t mine = m < mt ? cost_of(tiles_of<kPrefix, R, KT>(a, q, m)) : 0;
-      const int64_t upto = wave_scan(mine) * a.Hk;
-      const uint64_t beyond = __ballot(x < upto);
-      if (beyond != 0ull) {
-        const int of = __ffsll((unsigned long long)beyond) - 1;
-        c = __shfl(mine, of);
-        x -= __shfl(upto, of) - c * a.Hk;
-        p.m = uniform(m0 + of);
-        break;
-      }
-      x -= __shfl(upto, 63);
-    }
+    const int64_t each = cost_of(tiles_of<true, R, KT>(a, q, 0));
+    p.m = uniform((int)div64(p.pos, 1.0 / (double)(each * a.Hk)));
+    const int64_t x = p.pos - (int64_t)p.m * each * a.Hk;
+    p.h = uniform((int)div64(x, 1.0 / (double)each));
+    p.k = uniform((int)(x - p.h * each));
+    return p;
   }
-  p.h = uniform((int)div64(x, 1.0 / (double)c));
-  p.k = uniform((int)(x - p.h * c));
+  int64_t x;                                       // tiles into request r
+  if (one_wave) {
+    const int of = __ffsll((unsigned long long)__ballot(p.pos < upto * a.Hk)) - 1;
+    p.r = of;
+    x = p.pos - lane_of(upto - c, of) * a.Hk;
+    p.q.token0 = __builtin_amdgcn_readlane(q.token0, of);
+    p.q.n = __builtin_amdgcn_readlane(q.n, of);
+    p.q.p0 = __builtin_amdgcn_readlane(q.p0, of);
+    p.q.keys = __builtin_amdgcn_readlane(q.keys, of);
+  } else {
+    int64_t base = 0;
+    for (int r0 = 0; r0 < B; r0 += kThreads) {
+      int64_t all;
+      c = cost_at(r0 + tid, q);
+      const int64_t into = p.pos - base - block_scan<kWaves>(c, s_wave, all) * a.Hk;
+      if (into >= 0 && into < c * a.Hk) {          // one thread of one pass
+        s_found[0] = r0 + tid;
+        s_found[1] = into;
+      }
+      base += all * a.Hk;
+      if (p.pos < base) break;                     // uniform
+    }
+    __syncthreads();
+    p.r = uniform((int)s_found[0]);
+    x = s_found[1];
+    p.q = load_request<false>(a, p.r);
+  }
+  p.r = uniform(p.r);
+  p.q = uniform_request(p.q);
+  const int mt = row_tiles(a, p.q, R);
+  for (int m0 = 0; m0 < mt; m0 += 64) {            // every wave alike
+    const int m = m0 + lane;
+    const int64_t mine = m < mt ? cost_of(tiles_of<false, R, KT>(a, p.q, m)) : 0;
+    const int64_t all = wave_scan(mine);
+    const uint64_t beyond = __ballot(x < all * a.Hk);
+    if (beyond != 0ull) {
+      const int of = __ffsll((unsigned long long)beyond) - 1;
+      const int64_t each = lane_of(mine, of);
+      x -= (lane_of(all, of) - each) * a.Hk;
+      p.m = m0 + of;
+      p.h = uniform((int)div64(x, 1.0 / (double)each));
+      p.k = uniform((int)(x - p.h * each));
+      break;
+    }
+    x -= lane_of(all, 63) * a.Hk;
+  }
   return p;
 }
 
@@ -418,10 +475,16 @@ struct KernelArgs {
   AttentionArgs a;
   Parts parts;
 };
-__device__ __forceinline__ const KernelArgs* fresh_args() {
-  uint64_t p = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
-  asm volatile("" : "+s"(p));
-  return (const KernelArgs*)p;
+__device__ __forceinline__ KernelArgs fresh_args() {
+  typedef const __attribute__((address_space(4))) uint32_t* Words;   // scalar loads
+  Words w = (Words)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(w));
+  struct Raw {
+    uint32_t w[sizeof(KernelArgs) / 4];
+  } raw;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(KernelArgs) / 4; ++i) raw.w[i] = w[i];
+  return __builtin_bit_cast(KernelArgs, raw);
 }
 
 // score factor and query sign: queries are negated (exactly) where the factor
@@ -604,10 +667,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
   const float c = fac.c;
 
   while (at.pos < at.end) {
-    const Request q = load_request<kPrefix>(a, at.r);
+    const Request q = at.q;
     const int mt = row_tiles(a, q, R);
-    if (at.m >= mt) {                              // a request without queries
-      ++at.r;
+    if (at.m >= mt) {                              // done, or without queries
+      at.q = uniform_request(load_request<kPrefix>(a, ++at.r));
       at.m = at.h = at.k = 0;
       continue;
     }
@@ -796,8 +859,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
       }
     }
     __syncthreads();
-    const KernelArgs* fr = fresh_args();
-    const Parts parts = fr->parts;
+    const KernelArgs fr = fresh_args();
+    const Parts parts = fr.parts;
     const Target to = target_of(at, k1, cost, wg);
     // a thread takes 4 values of a row at a time
     constexpr int kVec = D / 4;
@@ -823,12 +886,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
       const int head = at.h * a.G + rr - i * a.G;
       const int64_t flat = token * a.Hq + head;
       if (to.whole && !kJoin) {
-        const float inv = ll == 0.0f ? 0.0f : fr->a.v_scale[0] / ll;
+        const float inv = ll == 0.0f ? 0.0f : fr.a.v_scale[0] / ll;
         const uint32_t w0 = pack_bf16(acc[0] * inv, acc[1] * inv);
         const uint32_t w1 = pack_bf16(acc[2] * inv, acc[3] * inv);
-        *reinterpret_cast<uint2*>(fr->a.out + token * fr->a.ld_out + (int64_t)head * D + d) =
+        *reinterpret_cast<uint2*>(fr.a.out + token * fr.a.ld_out + (int64_t)head * D + d) =
             make_uint2(w0, w1);
-        if (fr->a.lse && d == 0) fr->a.lse[flat] = (base + __builtin_log2f(ll)) * kLn2;
+        if (fr.a.lse && d == 0) fr.a.lse[flat] = (base + __builtin_log2f(ll)) * kLn2;
       } else {
         const int part_row = to.slot * R + row;
         float* po = to.whole ? parts.whole_o + flat * D : parts.o + (int64_t)part_row * D;
@@ -896,7 +959,6 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
   __shared__ __attribute__((aligned(16))) int s_slot[8][KT];   // of tile k in s_slot[k % 8]
   __shared__ int s_nan[2];                         // the last tile staged there with a NaN value
   __shared__ int64_t s_wave[kWaves], s_found[2];
-  const AttentionArgs& a = args.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int n = lane & 31, g = lane >> 5;
   const bool second = wave >= kWaves / 2;          // group
@@ -905,10 +967,10 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
   const int wgs = gridDim.x;
   const int wg = wgs % 8 == 0 ? (int)(blockIdx.x % 8) * (wgs / 8) + (int)(blockIdx.x / 8)
                               : (int)blockIdx.x;
-  Place at = find_share<kPrefix, R, KT, kWaves, 1>(a, wg, wgs, s_wave, s_found);
+  Place at = find_share<kPrefix, R, KT, kWaves, 1>(args.a, wg, wgs, s_wave, s_found);
   if (!kJoin && tid == 0) args.parts.split[wg].parts = 0;
-  const uint32_t stride = (uint32_t)a.Hk * D;
-  const Factor fac = factor_of(a);
+  const uint32_t stride = (uint32_t)args.a.Hk * D;
+  const Factor fac = factor_of(args.a);
   const float c = fac.c;
 
   // LDS places of this thread in buffers 0.  Reads: piece of k step 0 of row n of
@@ -929,10 +991,11 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
                         ((y_v >> 1) ^ ((r0_v ^ (r0_v >> 3)) & 7)) * 16 + (y_v & 1) * 8;
 
   while (at.pos < at.end) {
-    const Request q = load_request<kPrefix>(a, at.r);
+    const AttentionArgs a = fresh_args().a;        // see there
+    const Request q = at.q;
     const int mt = row_tiles(a, q, R);
-    if (at.m >= mt) {
-      ++at.r;
+    if (at.m >= mt) {                              // done, or without queries
+      at.q = uniform_request(load_request<kPrefix>(a, ++at.r));
       at.m = at.h = at.k = 0;
       continue;
     }
@@ -1345,8 +1408,8 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
     }
     l = sum_xor32(l);
 
-    const KernelArgs* fr = fresh_args();
-    const Parts parts = fr->parts;
+    const KernelArgs fr = fresh_args();
+    const Parts parts = fr.parts;
     const Target to = target_of(at, k1, cost, wg);
     if (mine) {
       const int64_t token = q.token0 + i_n;
@@ -1365,8 +1428,8 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
           }
       }
       if (to.whole && !kJoin) {
-        const float inv = l == 0.0f ? 0.0f : fr->a.v_scale[0] / l;
-        uint16_t* po = fr->a.out + token * fr->a.ld_out + (int64_t)head * D + g * (D / 2);
+        const float inv = l == 0.0f ? 0.0f : fr.a.v_scale[0] / l;
+        uint16_t* po = fr.a.out + token * fr.a.ld_out + (int64_t)head * D + g * (D / 2);
 #pragma unroll
         for (int b = 0; b < OB; ++b)
 #pragma unroll
@@ -1377,7 +1440,7 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
               w[e] = pack_bf16(o[b][i + 2 * e] * inv, o[b][i + 2 * e + 1] * inv);
             *reinterpret_cast<uint4*>(po + 16 * b + i) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        if (fr->a.lse && g == 0) fr->a.lse[flat] = (base_of(m) + __builtin_log2f(l)) * kLn2;
+        if (fr.a.lse && g == 0) fr.a.lse[flat] = (base_of(m) + __builtin_log2f(l)) * kLn2;
       } else {
         const int part_row = to.slot * R + row;
         float* po = (to.whole ? parts.whole_o + flat * D : parts.o + (int64_t)part_row * D) +
