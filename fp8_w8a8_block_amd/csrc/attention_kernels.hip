@@ -475,6 +475,12 @@ struct KernelArgs {
   AttentionArgs a;
   Parts parts;
 };
+template <typename T>
+__device__ __forceinline__ T* in_global(T* p) {    // not in LDS or scratch
+  const auto* any = (const __attribute__((address_space(0))) void*)p;
+  __builtin_assume(!__builtin_amdgcn_is_shared(any) && !__builtin_amdgcn_is_private(any));
+  return p;
+}
 __device__ __forceinline__ KernelArgs fresh_args() {
   typedef const __attribute__((address_space(4))) uint32_t* Words;   // scalar loads
   Words w = (Words)__builtin_amdgcn_kernarg_segment_ptr();
@@ -484,7 +490,26 @@ __device__ __forceinline__ KernelArgs fresh_args() {
   } raw;
 #pragma unroll
   for (unsigned i = 0; i < sizeof(KernelArgs) / 4; ++i) raw.w[i] = w[i];
-  return __builtin_bit_cast(KernelArgs, raw);
+  KernelArgs k = __builtin_bit_cast(KernelArgs, raw);
+  k.a.q = in_global(k.a.q);
+  k.a.kc = in_global(k.a.kc);
+  k.a.vc = in_global(k.a.vc);
+  k.a.table = in_global(k.a.table);
+  k.a.lens = in_global(k.a.lens);
+  k.a.offsets = in_global(k.a.offsets);
+  k.a.prefix_table = in_global(k.a.prefix_table);
+  k.a.prefix_len = in_global(k.a.prefix_len);
+  k.a.v_scale = in_global(k.a.v_scale);
+  k.a.out = in_global(k.a.out);
+  k.a.lse = in_global(k.a.lse);
+  k.parts.ml = in_global(k.parts.ml);
+  k.parts.o = in_global(k.parts.o);
+  k.parts.split = in_global(k.parts.split);
+  k.parts.where = in_global(k.parts.where);
+  k.parts.reset = in_global(k.parts.reset);
+  k.parts.whole_ml = in_global(k.parts.whole_ml);
+  k.parts.whole_o = in_global(k.parts.whole_o);
+  return k;
 }
 
 // score factor and query sign: queries are negated (exactly) where the factor
@@ -1020,9 +1045,11 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
 #pragma unroll
       for (int i = 0; i < KS; ++i) qf[i] = load_query(p + 16 * i, fac.flip);
     }
-    const int32_t* table = kPrefix ? a.prefix_table : a.table + (int64_t)at.r * a.ld_table;
-    const uint8_t* vc = a.vc + (int64_t)at.h * D;
-    const uint8_t* codes_k = a.kc + (int64_t)at.h * D + (tid % TK) * (4 * KW);   // this thread's
+    // from the kernel's own parameters, which are known to point to memory
+    const int32_t* table =
+        kPrefix ? args.a.prefix_table : args.a.table + (int64_t)at.r * a.ld_table;
+    const uint8_t* vc = args.a.vc + (int64_t)at.h * D;
+    const uint8_t* codes_k = args.a.kc + (int64_t)at.h * D + (tid % TK) * (4 * KW);   // this thread's
     const uint8_t* codes_v = vc + x_v * (4 * VW);
     const int count = tl.count();
     const int kend = k1 < count ? k1 : count;
@@ -1412,9 +1439,6 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
     const Parts parts = fr.parts;
     const Target to = target_of(at, k1, cost, wg);
     if (mine) {
-      const int64_t token = q.token0 + i_n;
-      const int head = at.h * a.G + row0 + row - i_n * a.G;
-      const int64_t flat = token * a.Hq + head;
       bool any = false;
 #pragma unroll
       for (int w = 0; w < D / 64; ++w) any |= nans.w[w] != 0u;
@@ -1427,31 +1451,78 @@ __global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attentio
             o[b][i] = (nans.w[bit / 32] >> (bit % 32)) & 1u ? __builtin_nanf("") : o[b][i];
           }
       }
-      if (to.whole && !kJoin) {
-        const float inv = l == 0.0f ? 0.0f : fr.a.v_scale[0] / l;
-        uint16_t* po = fr.a.out + token * fr.a.ld_out + (int64_t)head * D + g * (D / 2);
+      const int64_t flat = (int64_t)(q.token0 + i_n) * fr.a.Hq + at.h * a.G + row0 + row - i_n * a.G;
+      if (g == 0) {
+        if (!to.whole || kJoin) note_row<kPrefix, kJoin>(parts, to, flat, to.slot * R + row, m, l);
+        else if (fr.a.lse) fr.a.lse[flat] = (base_of(m) + __builtin_log2f(l)) * kLn2;
+      }
+    }
+    // A lane holds a row, and its stores would touch 64 lines each; the wave's
+    // part of the staging buffers, which all waves are done with, turns them into
+    // stores of whole rows, 16-byte pieces XORed with the row as above.
+    uint8_t* turn = s_kv + wave * (4 * kBuf / kWaves);
+    constexpr int kTurn = 4 * kBuf / kWaves / 32;  // bytes of a row there
+    const auto out_row = [&](int r) {              // where row r of the wave goes: token, head
+      const int rho = row0 + wave * 32 + r, i = (int)div32((uint32_t)rho, a.inv_G);
+      return make_int2(q.token0 + i, at.h * a.G + rho - i * a.G);
+    };
+    if (to.whole && !kJoin) {
+      const float inv = l == 0.0f ? 0.0f : fr.a.v_scale[0] / l;
+      constexpr int kPieces16 = D * 2 / 16;        // of a row of bf16
+      static_assert(D * 2 <= kTurn, "a row fits");
 #pragma unroll
-        for (int b = 0; b < OB; ++b)
+      for (int b = 0; b < OB; ++b)
 #pragma unroll
-          for (int i = 0; i < 16; i += 8) {
-            uint32_t w[4];
+        for (int i = 0; i < 16; i += 8) {
+          const int piece = g * (kPieces16 / 2) + 2 * b + i / 8;
+          *reinterpret_cast<uint4*>(turn + n * kTurn + (piece ^ (n & 7)) * 16) =
+              make_uint4(pack_bf16(o[b][i] * inv, o[b][i + 1] * inv),
+                         pack_bf16(o[b][i + 2] * inv, o[b][i + 3] * inv),
+                         pack_bf16(o[b][i + 4] * inv, o[b][i + 5] * inv),
+                         pack_bf16(o[b][i + 6] * inv, o[b][i + 7] * inv));
+        }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+      for (int x = 0; x < 32 * kPieces16 / 64; ++x) {
+        const int r = (x * 64 + lane) / kPieces16, piece = (x * 64 + lane) % kPieces16;
+        const uint4 v = *reinterpret_cast<const uint4*>(turn + r * kTurn + (piece ^ (r & 7)) * 16);
+        if (wave * 32 + r < rows) {
+          const int2 th = out_row(r);
+          *reinterpret_cast<uint4*>(fr.a.out + (int64_t)th.x * fr.a.ld_out + (int64_t)th.y * D +
+                                    piece * 8) = v;
+        }
+      }
+    } else {
+      constexpr int kPasses = D * 4 / kTurn > 0 ? D * 4 / kTurn : 1;
+      constexpr int kRow = D / kPasses;            // values of a row in a pass, half per g
+      constexpr int kPieces32 = kRow / 4;
+      static_assert(kRow * 4 <= kTurn && OB % kPasses == 0, "a pass fits");
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16(o[b][i + 2 * e] * inv, o[b][i + 2 * e + 1] * inv);
-            *reinterpret_cast<uint4*>(po + 16 * b + i) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int y = 0; y < kPasses; ++y) {
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int b = 0; b < OB / kPasses; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const f32x16& v = o[y * (OB / kPasses) + b];
+            const int piece = g * (kPieces32 / 2) + 4 * b + i / 4;
+            *reinterpret_cast<float4*>(turn + n * kTurn + (piece ^ (n & 7)) * 16) =
+                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
-        if (fr.a.lse && g == 0) fr.a.lse[flat] = (base_of(m) + __builtin_log2f(l)) * kLn2;
-      } else {
-        const int part_row = to.slot * R + row;
-        float* po = (to.whole ? parts.whole_o + flat * D : parts.o + (int64_t)part_row * D) +
-                    g * (D / 2);
-#pragma unroll
-        for (int b = 0; b < OB; ++b)
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(po + 16 * b + i) =
-                make_float4(o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]);
-        if (g == 0) note_row<kPrefix, kJoin>(parts, to, flat, part_row, m, l);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int x = 0; x < 32 * kPieces32 / 64; ++x) {
+          const int r = (x * 64 + lane) / kPieces32, piece = (x * 64 + lane) % kPieces32;
+          const float4 v =
+              *reinterpret_cast<const float4*>(turn + r * kTurn + (piece ^ (r & 7)) * 16);
+          if (wave * 32 + r < rows) {
+            const int2 th = out_row(r);
+            float* po = to.whole ? parts.whole_o + ((int64_t)th.x * fr.a.Hq + th.y) * D
+                                 : parts.o + (int64_t)(to.slot * R + wave * 32 + r) * D;
+            const int half = piece / (kPieces32 / 2), in = piece % (kPieces32 / 2);
+            *reinterpret_cast<float4*>(po + half * (D / 2) + y * (kRow / 2) + 4 * in) = v;
+          }
+        }
       }
     }
     note_item<kPrefix, kJoin>(parts, to, q, row0, rows, at.h, wg);
