@@ -9,7 +9,7 @@
 // Numbers.  E4M3 codes convert exactly to bf16 and to fp16 (4 significant
 // bits, 2^-9 .. 448), queries are bf16, so <q, K_j> is a sum of exact products
 // on the bf16 matrix instruction with fp32 accumulation, and nothing of the
-// scores is rounded below fp32.  P = exp(s - m) <= 1 goes to fp16, whose 11
+// scores is rounded below fp32.  P = exp(s - m) <= 2^8 goes to fp16, whose 11
 // bits keep its rounding (2^-11 relative, 2^-25 absolute below 2^-14) an order
 // under the bf16 output's; O is fp32, and l sums the fp32 values.  exp(x) is
 // exp2(x log2 e), the factor folded into the score scale.
@@ -375,12 +375,8 @@ __device__ __forceinline__ Place find_share(const AttentionArgs& a, int wg, int 
 }
 
 // ---- paging ----------------------------------------------------------------------
-// The table's entry for key j of a request (-1 behind the keys), and the cache
-// slot that it names, -1 where no block is mapped.  Two steps, so that the load
-// can be under way while other work is done.
-__device__ __forceinline__ int entry_of(const int32_t* table, int j, int keys, double inv_page) {
-  return j < keys ? table[div32((uint32_t)j, inv_page)] : -1;
-}
+// The cache slot of key j, whose block the table's entry names, -1 where none is
+// mapped.  The entry is read ahead, while other work is done.
 __device__ __forceinline__ int slot_of(int entry, int j, int page, double inv_page,
                                        int num_blocks) {
   const int i = (int)div32((uint32_t)j, inv_page);
@@ -476,7 +472,7 @@ struct KernelArgs {
   Parts parts;
 };
 template <typename T>
-__device__ __forceinline__ T* in_global(T* p) {    // not in LDS or scratch
+__device__ __forceinline__ T* in_global(T* p) {    // tells that p is not in LDS or scratch
   const auto* any = (const __attribute__((address_space(0))) void*)p;
   __builtin_assume(!__builtin_amdgcn_is_shared(any) && !__builtin_amdgcn_is_private(any));
   return p;
@@ -962,13 +958,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
 // leaves each lane with D / 2 values in a row to store.
 constexpr int tile_keys(int D) { return D == 64 ? 128 : 64; }
 
-// waves of a workgroup: D = 256 needs a whole SIMD's registers for one wave
-constexpr int tile_waves(int D) { return D == 256 ? 4 : 8; }
+constexpr int kTileWaves = 8;
 
 template <int D, bool kPrefix, bool kJoin>
-__global__ __launch_bounds__(tile_waves(D) * 64, D == 256 ? 1 : 2) void attention_tile_kernel(
-    KernelArgs args) {
-  constexpr int kWaves = tile_waves(D);
+__global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(KernelArgs args) {
+  static_assert(D <= 128, "a wave's registers");
+  constexpr int kWaves = kTileWaves;
   constexpr int R = kWaves * 32, KT = tile_keys(D);
   constexpr int KS = D / 16;                       // k steps of K Q^T
   constexpr int OB = D / 32;                       // 32-row blocks of O^T
@@ -1690,19 +1685,27 @@ int compute_units() {
   return n;
 }
 
-// Rows per request, on average, from which the large row tiles are used.
-bool many_rows(int64_t T, int64_t B, int64_t G) { return T * G > 32 * B; }
+// Whether B requests' T query tokens take the 256-row tiles: from 48 rows per
+// request on average.  Measured (us, 16-row against 256-row tiles): 64 requests
+// of 2048 keys, D = 128, Hk = 8: 64 / 147 at 16 rows, 110 / 143 at 32, 151 / 144
+// at 48, 199 / 142 at 64; 4 requests of 16000: 73 / 92 at 32, 108 / 105 at 64;
+// 32 requests of 2048, D = 64: 38 / 50 at 32, 69 / 52 at 64.  A shared prefix is
+// one request of all rows: of 32768 keys, 59 / 64 at 48 rows, 103 / 64 at 96.
+// D = 256 has the 16-row tiles only: 32 rows of O and Q fill a wave's registers
+// there, and 256-row tiles that spill took 1336 us where these take 199 (32
+// requests of 256 rows, 2048 keys).
+bool many_rows(int64_t T, int64_t B, int64_t G, int64_t D) { return D < 256 && T * G > 48 * B; }
 
 struct Shape {
   bool tiles;                   // large row tiles
   int wgs, R;
 };
 
-Shape shape_of(bool tiles, int D) {
+Shape shape_of(bool tiles, int64_t D) {
   const int cus = compute_units();
   Shape s;
   s.tiles = tiles;
-  s.R = tiles ? tile_waves(D) * 32 : kRowsD;
+  s.R = tiles ? kTileWaves * 32 : kRowsD;
   s.wgs = tiles ? cus : (D == 256 ? cus : 2 * cus);
   return s;
 }
@@ -1733,10 +1736,13 @@ Parts lay_out(uint8_t* ws, size_t& at, const Shape& s, int64_t D, int64_t rows_j
 template <int D, bool kPrefix, bool kJoin>
 void launch_main(const AttentionArgs& a, const Parts& p, const Shape& s, hipStream_t st) {
   const KernelArgs k = {a, p};
-  if (s.tiles)
-    hipLaunchKernelGGL((attention_tile_kernel<D, kPrefix, kJoin>), dim3(s.wgs),
-                       dim3(tile_waves(D) * 64), 0, st, k);
-  else if (a.page % 4 == 0)
+  if constexpr (D < 256)
+    if (s.tiles) {
+      hipLaunchKernelGGL((attention_tile_kernel<D, kPrefix, kJoin>), dim3(s.wgs),
+                         dim3(kTileWaves * 64), 0, st, k);
+      return;
+    }
+  if (a.page % 4 == 0)
     hipLaunchKernelGGL((attention_rows_kernel<D, kPrefix, kJoin, true>), dim3(s.wgs),
                        dim3(kThreads), 0, st, k);
   else
@@ -1748,7 +1754,7 @@ template <int D>
 hipError_t launch_d(const AttentionArgs& a, hipStream_t st) {
   size_t at = 0;
   if (!a.prefix_len) {
-    const Shape s = shape_of(many_rows(a.T, a.B, a.G), D);
+    const Shape s = shape_of(many_rows(a.T, a.B, a.G, D), D);
     const Parts p = lay_out(a.ws, at, s, D, 0);
     launch_main<D, false, false>(a, p, s, st);
     hipError_t e = hipGetLastError();
@@ -1758,8 +1764,8 @@ hipError_t launch_d(const AttentionArgs& a, hipStream_t st) {
     return hipGetLastError();
   }
   const int64_t rows = (int64_t)a.T * a.Hq;
-  const Shape s1 = shape_of((int64_t)a.T * a.G > kRowsD, D);
-  const Shape s2 = shape_of(many_rows(a.T, a.B, a.G), D);
+  const Shape s1 = shape_of(many_rows(a.T, 1, a.G, D), D);
+  const Shape s2 = shape_of(many_rows(a.T, a.B, a.G, D), D);
   Parts p1 = lay_out(a.ws, at, s1, D, rows), p2 = lay_out(a.ws, at, s2, D, rows);
   p1.reset = p2.where;
   launch_main<D, true, true>(a, p1, s1, st);
@@ -1778,10 +1784,10 @@ size_t attention_workspace(bool prefix, int64_t T, int64_t B, int64_t Hq, int64_
   const int64_t G = Hq / Hk;
   size_t at = 0;
   if (!prefix) {
-    lay_out(nullptr, at, shape_of(many_rows(T, B, G), (int)D), D, 0);
+    lay_out(nullptr, at, shape_of(many_rows(T, B, G, D), D), D, 0);
   } else {
-    lay_out(nullptr, at, shape_of(T * G > kRowsD, (int)D), D, T * Hq);
-    lay_out(nullptr, at, shape_of(many_rows(T, B, G), (int)D), D, T * Hq);
+    lay_out(nullptr, at, shape_of(many_rows(T, 1, G, D), D), D, T * Hq);
+    lay_out(nullptr, at, shape_of(many_rows(T, B, G, D), D), D, T * Hq);
   }
   return at;
 }
