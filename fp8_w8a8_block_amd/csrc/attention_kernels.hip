@@ -606,6 +606,13 @@ __device__ __forceinline__ void note_row(const Parts& parts, const Target& t, in
 // bytes of key n), and for V lane (n, g) reads bytes n D/16 .. of the 8 keys
 // that its P values stand for, transposes them in registers and converts.  The
 // next unit's 8 KB (D = 128) are in flight while one is computed.
+//
+// Bound by the reads of the cache.  Two workgroups per CU (D = 256, whose waves
+// need more registers: one) keep 64 KB in flight on a CU; loads that do not stay
+// in the L2, each code being read once, gain 3 %.  64 requests of 1000 .. 8192
+// keys (603 MB, D = 128) take 128 us, 4.7 TB/s; a plain sum over as many bytes
+// takes 105.  One request of 131071 keys (268 MB) takes 64 us: 52 for the keys
+// and 9 for the launch that joins its 512 parts.
 constexpr int kRowsD = 16;
 constexpr int kKeysD = 128;
 
@@ -931,9 +938,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
 }
 
 // ---- many rows: 256-row tiles ----------------------------------------------------
-// One workgroup of kWaves waves, 32 rows each; a key tile is 64 keys, staged in
-// LDS once for all waves: K as bf16 [key][D], V as fp16 [d][key], both converted
-// on the way in (V transposed in registers, 4 keys at a time), two buffers each.
+// One workgroup of 8 waves, 32 rows each; a key tile is 64 keys (128 for D = 64),
+// staged in LDS once for all waves: K as bf16 [key][D], V as fp16 [d][key], both
+// converted on the way in (V transposed in registers, 4 keys at a time), two
+// buffers each.  256 rows a tile, so that the conversion of a code (which costs as
+// much as its product with 32 rows) and its read are shared by as many rows as the
+// registers of a CU hold.
 // 32 x 32 x 16 products: lane (n, g) with n = lane % 32 holds row n of S^T and O^T.
 //
 // Two phases alternate: products (V j with P j, then K j + 1 with Q) and softmax
@@ -951,6 +961,17 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
 // The exponents' base m moves only where a row's maximum passes it by 2^8 (P then
 // reaches 256, which fp16 holds as exactly as 1), so that O is rescaled a few
 // times per item and not in every other tile.
+//
+// Bound by the two phases' sum.  Measured at D = 128, per tile of 64 keys and wave:
+// products 1870 cycles (1024 of them the matrix unit's, the rest operands from LDS
+// and the staging in between), softmax 1430, waits at the barriers 430; two waves
+// on a SIMD then use 55 % of its matrix unit.  An item's start and end, 23000
+// cycles where nothing overlaps, weigh as 6 tiles.  8192 tokens of 3 requests
+// behind up to 4096 cached ones (32 + 8 heads of 128, 519 GFLOP in visible pairs)
+// take 620 .. 655 us, 0.8 PFLOP/s, where a large bf16 matrix product reaches 1.42.
+// 8001 tokens with a window of 1000 (64 + 8 heads of 64, 132 GFLOP) take 318:
+// tiles that the mask cuts are computed whole, and with D = 64 a key's softmax
+// stands beside half the products.
 //
 // LDS rows are cut into 16-byte pieces whose index is XORed with the row's, so
 // that the 32 rows that one read names lie in different banks.  O^T's rows

@@ -13,7 +13,8 @@
 // block that this step hands out reads the free list, not the table entry that
 // another workgroup may be writing, so no workgroup waits for another.  The
 // sums cost a few microseconds of latency per 1024 requests, less than a
-// second launch that would read them.
+// second launch that would read them.  Bound by that latency and the launch's:
+// 256 decoding requests take 4.9 us, 65536 tokens of 96 prompts (1 MB) 6.0.
 #include "attention_launch.h"
 
 namespace fp8k {
@@ -34,7 +35,7 @@ __device__ __forceinline__ uint32_t blocks_of(uint32_t tokens, uint32_t page) {
 }
 
 // kPer requests per thread and pass: one while the batch has at most 256
-// (a shorter scan and search: 6.3 -> 5 us for 256 decoding requests), else 4.
+// (a shorter scan and search: 6.3 -> 4.9 us for 256 decoding requests), else 4.
 template <int kPer>
 __global__ __launch_bounds__(kThreads) void slot_map_kernel(SlotMapArgs a) {
   constexpr int kChunk = kThreads * kPer;     // requests per pass
