@@ -1617,9 +1617,9 @@ __device__ __forceinline__ void add_parts(Sum<D>& s, const float* ml, const floa
 
 template <int D>
 __device__ __forceinline__ void write_row(const AttentionArgs& a, const Sum<D>& s, float base,
-                                          int64_t token, int head) {
+                                          float v_scale, int64_t token, int head) {
   const int lane = threadIdx.x & 63;
-  const float inv = s.l == 0.0f ? 0.0f : a.v_scale[0] / s.l;
+  const float inv = s.l == 0.0f ? 0.0f : v_scale / s.l;
   uint16_t* p = a.out + token * a.ld_out + (int64_t)head * D + lane * (D / 64);
 #pragma unroll
   for (int i = 0; i < D / 64; i += 2) {
@@ -1630,43 +1630,87 @@ __device__ __forceinline__ void write_row(const AttentionArgs& a, const Sum<D>& 
   if (a.lse && lane == 0) a.lse[token * a.Hq + head] = (base + __builtin_log2f(s.l)) * kLn2;
 }
 
-// Items that shares cut: block (w, y) joins rows y, y + gridDim.y, .. of the
-// item that starts in workgroup w's share.  With many parts the four waves
-// share a row's parts, else each takes rows of its own.
+// Items that shares cut: the blocks (w, y) join the rows of the item that starts
+// in workgroup w's share.  With many parts the four waves of a block share a row's
+// parts.  With few, 16 lanes take a row, so that a wave has the loads of four rows
+// in flight: the time is that of the chain of loads (descriptor, m, O), and with
+// one row per wave the join of a prefill's 512 parts (84 MB) took 19 us longer.
+constexpr int kFewParts = 8;
+
 template <int D>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs a, Parts parts,
                                                                   int R) {
   __shared__ float s_l[4], s_o[4][D];
   const Split sp = parts.split[blockIdx.x];
   if (sp.parts == 0) return;
+  const float v_scale = a.v_scale[0];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const bool wide = sp.parts > 8;
-  const int first = wide ? blockIdx.y : blockIdx.y * 4 + wave;
-  const int step = wide ? gridDim.y : gridDim.y * 4;
-  for (int row = first; row < sp.rows; row += step) {
-    const int64_t f = ((int64_t)2 * blockIdx.x + 1) * R + row;
-    const float base = base_of(parts_max(parts.ml, f, sp.parts, R));
+  const int64_t f0 = ((int64_t)2 * blockIdx.x + 1) * R;
+  if (sp.parts <= kFewParts) {
+    const int c = lane & 15;                       // values 4 c .. 4 c + 3 of each 64
+    for (int r0 = (blockIdx.y * 4 + wave) * 4; r0 < sp.rows; r0 += gridDim.y * 16) {
+      const int row = r0 + (lane >> 4);
+      if (row >= sp.rows) continue;
+      float2 ml[kFewParts];
+      float m = FP8_NEG_INF;
+#pragma unroll
+      for (int j = 0; j < kFewParts; ++j)
+        if (j < sp.parts)
+          ml[j] = *reinterpret_cast<const float2*>(parts.ml + part_row(f0 + row, j, R) * 2);
+#pragma unroll
+      for (int j = 0; j < kFewParts; ++j)
+        if (j < sp.parts) m = __builtin_fmaxf(m, ml[j].x);
+      const float base = base_of(m);
+      float l = 0.0f;
+      float4 o[D / 64];
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int j = 0; j < kFewParts; ++j)
+        if (j < sp.parts) {
+          const float w = __builtin_amdgcn_exp2f(ml[j].x - base);
+          l = __builtin_fmaf(ml[j].y, w, l);
+          const float* p = parts.o + part_row(f0 + row, j, R) * D + 4 * c;
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            const float4 x = *reinterpret_cast<const float4*>(p + 64 * i);
+            o[i].x = __builtin_fmaf(x.x, w, o[i].x);
+            o[i].y = __builtin_fmaf(x.y, w, o[i].y);
+            o[i].z = __builtin_fmaf(x.z, w, o[i].z);
+            o[i].w = __builtin_fmaf(x.w, w, o[i].w);
+          }
+        }
+      const float inv = l == 0.0f ? 0.0f : v_scale / l;
+      const int rho = sp.row0 + row, i_n = (int)div32((uint32_t)rho, a.inv_G);
+      const int64_t token = sp.token0 + i_n;
+      const int head = sp.head * a.G + rho - i_n * a.G;
+      uint16_t* out = a.out + token * a.ld_out + (int64_t)head * D + 4 * c;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        *reinterpret_cast<uint2*>(out + 64 * i) = make_uint2(pack_bf16(o[i].x * inv, o[i].y * inv),
+                                                             pack_bf16(o[i].z * inv, o[i].w * inv));
+      if (a.lse && c == 0) a.lse[token * a.Hq + head] = (base + __builtin_log2f(l)) * kLn2;
+    }
+    return;
+  }
+  for (int row = blockIdx.y; row < sp.rows; row += gridDim.y) {
+    const float base = base_of(parts_max(parts.ml, f0 + row, sp.parts, R));
     Sum<D> s = {};
-    if (wide)
-      add_parts<D, 8>(s, parts.ml, parts.o, f, sp.parts, R, base, wave, 4);
-    else
-      add_parts<D, 2>(s, parts.ml, parts.o, f, sp.parts, R, base, 0, 1);
-    if (wide) {
-      __syncthreads();
-      if (lane == 0) s_l[wave] = s.l;
+    add_parts<D, 16>(s, parts.ml, parts.o, f0 + row, sp.parts, R, base, wave, 4);
+    __syncthreads();
+    if (lane == 0) s_l[wave] = s.l;
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) s_o[wave][lane * (D / 64) + i] = s.o[i];
-      __syncthreads();
-      if (wave != 0) continue;
+    for (int i = 0; i < D / 64; ++i) s_o[wave][lane * (D / 64) + i] = s.o[i];
+    __syncthreads();
+    if (wave != 0) continue;
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        s.l += s_l[w];
+    for (int w = 1; w < 4; ++w) {
+      s.l += s_l[w];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) s.o[i] += s_o[w][lane * (D / 64) + i];
-      }
+      for (int i = 0; i < D / 64; ++i) s.o[i] += s_o[w][lane * (D / 64) + i];
     }
     const int rho = sp.row0 + row, i = (int)div32((uint32_t)rho, a.inv_G);
-    write_row<D>(a, s, base, sp.token0 + i, sp.head * a.G + rho - i * a.G);
+    write_row<D>(a, s, base, v_scale, sp.token0 + i, sp.head * a.G + rho - i * a.G);
   }
 }
 
@@ -1679,6 +1723,7 @@ __global__ __launch_bounds__(kThreads) void attention_prefix_join_kernel(Attenti
   if (flat >= (int64_t)a.T * a.Hq) return;
   const int2 w1 = p1.where[flat], w2 = p2.where[flat];
   if (w2.y < 0) return;                            // a row of no request
+  const float v_scale = a.v_scale[0];
   const float m1 = w1.y ? parts_max(p1.ml, w1.x, w1.y, R1) : p1.whole_ml[flat * 2];
   const float m2 = w2.y ? parts_max(p2.ml, w2.x, w2.y, R2) : p2.whole_ml[flat * 2];
   const float base = base_of(__builtin_fmaxf(m1, m2));
@@ -1688,7 +1733,7 @@ __global__ __launch_bounds__(kThreads) void attention_prefix_join_kernel(Attenti
   if (w2.y) add_parts<D, 2>(s, p2.ml, p2.o, w2.x, w2.y, R2, base, 0, 1);
   else add_row<D>(s, p2.whole_ml, p2.whole_o, flat, base);
   const int64_t token = flat / a.Hq;
-  write_row<D>(a, s, base, token, (int)(flat - token * a.Hq));
+  write_row<D>(a, s, base, v_scale, token, (int)(flat - token * a.Hq));
 }
 
 // ---- host ---------------------------------------------------------------------------
