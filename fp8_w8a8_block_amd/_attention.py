@@ -3,9 +3,13 @@ argument marshalling only, with the conventions of _lib.
 
 Every length, offset and table stays on the device; no call synchronizes, so
 a whole step can be captured in a graph.
+
+Arguments as they should be are read by _tensor_args (csrc/tensor_args.cpp), one
+call each; the checks written out here say what is wrong with the others.
 """
 
 import ctypes
+import importlib
 
 import torch
 
@@ -40,6 +44,19 @@ _SIGS = {
 _bound = None
 
 
+class _Unloaded:
+    """Loads _tensor_args in the first call's place, as lib() does the library: the
+    package is imported to build it."""
+
+    def __getattr__(self, name):
+        global _tensor_args
+        _tensor_args = importlib.import_module("._tensor_args", __package__)
+        return getattr(_tensor_args, name)
+
+
+_tensor_args = _Unloaded()
+
+
 def lib():
     """The loaded shared library with this header's argument types set, too."""
     global _bound
@@ -70,6 +87,9 @@ def _device_of(t, name):
 
 def _vector(t, name, dtype, device, n=None):
     """A contiguous 1-D device tensor (of n elements) -> its pointer."""
+    p = _tensor_args.vector(t, dtype, device, -1 if n is None else n)
+    if p is not None:
+        return p
     _on(t, name, dtype, device)
     if t.dim() != 1 or (n is not None and t.shape[0] != n):
         raise ValueError(f"{name} must be 1-D" + (f" of {n} elements" if n is not None else ""))
@@ -79,20 +99,24 @@ def _vector(t, name, dtype, device, n=None):
 
 
 def _heads(t, name, device):
-    """[T, H, D] bf16 with each token's H * D values contiguous -> (T, H, D, token stride)."""
+    """[T, H, D] bf16 with each token's H * D values contiguous
+    -> (pointer, T, H, D, token stride)."""
+    got = _tensor_args.heads(t, device)
+    if got is not None:
+        return got
     _on(t, name, torch.bfloat16, device)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, H, D]")
     T, H, D = t.shape
-    ld, sh, sd = t.stride()
-    if T * H * D == 0:
-        return T, H, D, H * D
-    if sd != 1 or (sh != D and H > 1):
+    if T * H * D > 0:
         raise ValueError(f"{name} must be [T, H, D] with contiguous heads")
-    return T, H, D, (ld if T > 1 else H * D)
+    return t.data_ptr(), T, H, D, H * D
 
 
 def _scale(t, name, device):
+    p = _tensor_args.vector(t, torch.float32, device, 1)
+    if p is not None:
+        return p
     _on(t, name, torch.float32, device)
     if t.numel() != 1:
         raise ValueError(f"{name} must hold one value")
@@ -101,6 +125,9 @@ def _scale(t, name, device):
 
 def _block_table(t, name, device, rows):
     """[rows, width] int32 with unit column stride -> (pointer, row stride, width)."""
+    got = _tensor_args.table(t, device, rows)
+    if got is not None:
+        return got
     _on(t, name, torch.int32, device)
     if t.dim() != 2 or t.shape[0] != rows:
         raise ValueError(f"{name} must be [{rows}, width]")
@@ -110,15 +137,25 @@ def _block_table(t, name, device, rows):
     return t.data_ptr(), (ld if rows > 1 else width), width
 
 
+def _matrix(t, name, dtype, device):
+    """A contiguous 2-D device tensor -> (pointer, rows, columns)."""
+    got = _tensor_args.matrix(t, dtype, device)
+    if got is None:
+        _on(t, name, dtype, device)
+        raise ValueError(f"{name} must be 2-D and contiguous")
+    return got
+
+
 def _caches(key_cache, value_cache, device):
-    """Both paged caches -> (blocks, block_size, H, D)."""
+    """Both paged caches -> (key pointer, value pointer, blocks, block_size, H, D)."""
+    got = _tensor_args.caches(key_cache, value_cache, device)
+    if got is not None:
+        return got
     for c, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
         _on(c, name, torch.uint8, device)
         if c.dim() != 4 or not c.is_contiguous():
             raise ValueError(f"{name} must be a contiguous [blocks, block_size, H, D] tensor")
-    if value_cache.shape != key_cache.shape:
-        raise ValueError("key_cache and value_cache shapes differ")
-    return key_cache.shape
+    raise ValueError("key_cache and value_cache shapes differ")
 
 
 def _raw_stream(device):
@@ -128,7 +165,7 @@ def _raw_stream(device):
 
 def _call(device, call):
     """Runs call() with `device` current."""
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         return call()
     with torch.cuda.device(device):
         return call()
@@ -185,30 +222,27 @@ def qk_norm_rope_cache(query, key, value, q_weight, k_weight, cos_sin, positions
     neighbours instead of halves.  Tokens whose position is outside the table
     are padding: their rows of query_out stay as they were."""
     dev = _device_of(query, "query")
-    T, Hq, D, ld_q = _heads(query, "query", dev)
-    Tk, Hk, Dk, ld_k = _heads(key, "key", dev)
-    Tv, Hv, Dv, ld_v = _heads(value, "value", dev)
+    q, T, Hq, D, ld_q = _heads(query, "query", dev)
+    k, Tk, Hk, Dk, ld_k = _heads(key, "key", dev)
+    v, Tv, Hv, Dv, ld_v = _heads(value, "value", dev)
     if Tk != T or Dk != D or Tv != T or Hv != Hk or Dv != D:
         raise ValueError("query, key and value shapes do not match")
-    nb, bs, Hc, Dc = _caches(key_cache, value_cache, dev)
+    kc, vc, nb, bs, Hc, Dc = _caches(key_cache, value_cache, dev)
     if Hc != Hk or Dc != D:
         raise ValueError("cache shapes do not match the tokens")
-    _on(cos_sin, "cos_sin", torch.float32, dev)
-    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be a contiguous [positions, rot_dim] tensor")
+    cs, max_pos, rot = _matrix(cos_sin, "cos_sin", torch.float32, dev)
     if query_out is None:
         query_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    To, Ho, Do, ld_o = _heads(query_out, "query_out", dev)
+    o, To, Ho, Do, ld_o = _heads(query_out, "query_out", dev)
     if To != T or Ho != Hq or Do != D:
         raise ValueError(f"query_out must be [{T}, {Hq}, {D}]")
-    max_pos, rot = cos_sin.shape
-    args = (query.data_ptr(), ld_q, key.data_ptr(), ld_k, value.data_ptr(), ld_v,
+    args = (q, ld_q, k, ld_k, v, ld_v,
             _vector(q_weight, "q_weight", torch.bfloat16, dev, D),
-            _vector(k_weight, "k_weight", torch.bfloat16, dev, D), float(eps), cos_sin.data_ptr(),
+            _vector(k_weight, "k_weight", torch.bfloat16, dev, D), float(eps), cs,
             max_pos, rot, int(bool(interleaved)),
             _vector(positions, "positions", torch.int64, dev, T),
             _vector(slot_mapping, "slot_mapping", torch.int64, dev, T), T, Hq, Hk, D,
-            query_out.data_ptr(), ld_o, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs,
+            o, ld_o, kc, vc, nb, bs,
             _scale(k_scale, "k_scale", dev), _scale(v_scale, "v_scale", dev))
     _check(_call(dev, lambda: lib().fp8_qk_norm_rope_cache(*args, _raw_stream(dev))))
     return query_out
@@ -225,8 +259,8 @@ def _attention(query, key_cache, value_cache, prefix, block_table, seq_lens, que
                v_scale, scale, window, sinks, out, lse, workspace):
     """Both attention calls; prefix: None or (prefix_table, prefix_len)."""
     dev = _device_of(query, "query")
-    T, Hq, D, ld_q = _heads(query, "query", dev)
-    nb, bs, Hk, Dc = _caches(key_cache, value_cache, dev)
+    q, T, Hq, D, ld_q = _heads(query, "query", dev)
+    kc, vc, nb, bs, Hk, Dc = _caches(key_cache, value_cache, dev)
     if Dc != D:
         raise ValueError("query and cache head sizes differ")
     lens = _vector(seq_lens, "seq_lens", torch.int32, dev)
@@ -242,15 +276,14 @@ def _attention(query, key_cache, value_cache, prefix, block_table, seq_lens, que
         batch = (*batch, int(window), int(sinks))
     if out is None:
         out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    To, Ho, Do, ld_o = _heads(out, "out", dev)
+    o, To, Ho, Do, ld_o = _heads(out, "out", dev)
     if To != T or Ho != Hq or Do != D:
         raise ValueError(f"out must be [{T}, {Hq}, {D}]")
     lse_ptr = None
     if lse is not None:
-        _on(lse, "lse", torch.float32, dev)
-        if lse.shape != (T, Hq) or not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous [{T}, {Hq}] tensor")
-        lse_ptr = lse.data_ptr()
+        lse_ptr, *shape = _matrix(lse, "lse", torch.float32, dev)
+        if shape != [T, Hq]:
+            raise ValueError(f"lse must be [{T}, {Hq}]")
 
     def call():
         l, ws = lib(), workspace
@@ -259,8 +292,7 @@ def _attention(query, key_cache, value_cache, prefix, block_table, seq_lens, que
             ws = torch.empty(n, dtype=torch.uint8, device=dev)
         ws_ptr, ws_len = _workspace(ws, dev)
         f = l.fp8_paged_attention if prefix is None else l.fp8_prefix_attention
-        return f(query.data_ptr(), ld_q, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs,
-                 *batch, out.data_ptr(), ld_o, lse_ptr, T, Hq, Hk, D, ws_ptr, ws_len,
+        return f(q, ld_q, kc, vc, nb, bs, *batch, o, ld_o, lse_ptr, T, Hq, Hk, D, ws_ptr, ws_len,
                  _raw_stream(dev))
 
     _check(_call(dev, call))

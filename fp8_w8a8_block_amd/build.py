@@ -1,5 +1,5 @@
 """Build libfp8w8a8.so (and bench.py's libhbmprobe.so) in-tree with hipcc
-for gfx950.
+for gfx950, and the binding's _tensor_args extension with the host compiler.
 
     python -m fp8_w8a8_block_amd.build        # or fp8_w8a8_block_amd.build.build()
 
@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +26,8 @@ SOURCES = ["abi.hip", "quant_kernels.hip", "gemm_kernels.hip", "kv_kernels.hip",
            "attention_abi.hip", "slot_kernels.hip", "rope_kernels.hip", "attention_kernels.hip"]
 PROBE_SOURCE = "hbm_probe.hip"                 # bench.py's HBM and matrix-unit references
 PROBE_LIB = os.path.join(PKG, "libhbmprobe.so")
+ARGS_SOURCE = "tensor_args.cpp"                # the binding's reader of tensor arguments
+ARGS_LIB = os.path.join(PKG, "_tensor_args.so")
 ARCH = "gfx950"
 
 
@@ -59,6 +62,25 @@ def _compile(src, verbose):
     return obj
 
 
+def _build_args(verbose):
+    """The extension module: host code against torch's own headers."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    tmp = ARGS_LIB + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, ARGS_SOURCE), "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {ARGS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, ARGS_LIB)
+
+
 def build(verbose=False):
     """Compile every HIP source for gfx950 and link the shared library."""
     os.makedirs(BUILD, exist_ok=True)
@@ -81,6 +103,7 @@ def build(verbose=False):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, PROBE_LIB)
+    _build_args(verbose)
     return LIB
 
 
