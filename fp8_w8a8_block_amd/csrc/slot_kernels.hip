@@ -133,18 +133,24 @@ __global__ __launch_bounds__(kThreads) void slot_map_kernel(SlotMapArgs a) {
       a.slots[t] = blk < 0 ? -1 : blk * (int64_t)page + (pos - i * page);
     }
 
-    // table entries of the pass's blocks, numbered as they are handed out
-    for (int64_t f = (int64_t)blockIdx.x * kThreads + tid; f < all_b;
-         f += (int64_t)gridDim.x * kThreads) {
+    // table entries of the pass's blocks, numbered as they are handed out; blocks
+    // behind a row's end are passed over together, however many lengths ask for
+    const int64_t stride = (int64_t)gridDim.x * kThreads;
+    for (int64_t f = (int64_t)blockIdx.x * kThreads + tid; f < all_b;) {
       int b = 0, e = kChunk;                  // last request whose first block is <= f
       while (e - b > 1) {
         const int m = (b + e) >> 1;
         if (s_first[m] <= f) b = m; else e = m;
       }
       const int64_t i = blocks_of((uint32_t)s_have_tokens[b], page) + (f - s_first[b]);
-      if (i < a.width)
+      if (i < a.width) {
         a.table[(r0 + b) * a.ld_table + i] =
             blk_base + f < a.num_free ? a.free_blocks[blk_base + f] : -1;
+        f += stride;
+      } else {
+        const int64_t next = b + 1 < kChunk ? s_first[b + 1] : all_b;
+        f += (next - f + stride - 1) / stride * stride;
+      }
     }
     tok_base += all_n;
     blk_base += all_b;

@@ -81,6 +81,21 @@ def test_unmapped_pages_and_huge_lengths():
     assert got[0].tolist() == [-1] * 4
 
 
+def test_lengths_that_no_table_holds():
+    """Blocks behind a row's end are counted, not walked: 2^31 of them in each of 300 rows."""
+    big, B, width = (1 << 31) - 1, 300, 4
+    free = np.arange(50, 60)
+    table = i32(np.full((B, width), 7))
+    got = fp8.kv_slot_map(i32([1] * B), i32([2] + [big] * (B - 1)), table, i32(free), 1, 6)
+    want = np.full((B, width), 7)                          # entry 0 was there
+    want[0, 1:3] = free[:2]
+    want[1, 1:] = free[2:5]
+    want[2:, 1:] = -1                                      # the list ended in the row before
+    assert np.array_equal(table.cpu().numpy(), want)
+    assert got[0].tolist() == [50, 51, 52, 53, 54, -1] and got[1].tolist() == [1, 2, 1, 2, 3, 4]
+    assert int(got[4]) == big
+
+
 def test_refusals():
     x, t = i32([1, 2]), i32([[0], [0]])
     with pytest.raises(TypeError):
