@@ -460,7 +460,7 @@ __device__ __forceinline__ Sight sight_of(const AttentionArgs& a, const Request&
   Sight s;
   s.hi = kPrefix ? q.keys - 1 : q.p0 + i;
   s.hi = s.hi < q.keys ? s.hi : q.keys - 1;
-  s.lo = !kPrefix && a.window > 0 ? q.p0 + i - a.window + 1 : 0;
+  s.lo = !kPrefix && a.window > 0 && q.p0 + i >= a.window ? q.p0 + i - a.window + 1 : 0;
   s.sinks = a.sinks;
   return s;
 }

@@ -168,6 +168,17 @@ def test_window_and_sinks(window, sinks):
     Batch(window, [(70, 300)], 4, 2, 128).check(window=window, sinks=sinks)
 
 
+def test_widest_window():
+    """A window and sinks of the largest number, with queries before position 0."""
+    big = (1 << 31) - 1
+    for D in (64, 128):
+        b = Batch(D, [(1, 40), (3, 1), (1, 0), (70, 9)], 8, 2, D)
+        b.check(window=big)
+        b.check(window=big, sinks=big)
+    b = Batch(7, [(90, 20), (200, 131)], 8, 2, 64)
+    b.check(window=big, sinks=3)
+
+
 def test_long_context():
     """One request over many shares, and a batch of more requests than a scan pass."""
     Batch(1, [(1, 20011)], 4, 1, 64).check()
