@@ -611,8 +611,8 @@ __device__ __forceinline__ void note_row(const Parts& parts, const Target& t, in
 // need more registers: one) keep 64 KB in flight on a CU; loads that do not stay
 // in the L2, each code being read once, gain 3 %.  64 requests of 1000 .. 8192
 // keys (603 MB, D = 128) take 128 us, 4.7 TB/s; a plain sum over as many bytes
-// takes 105.  One request of 131071 keys (268 MB) takes 64 us: 52 for the keys
-// and 9 for the launch that joins its 512 parts.
+// takes 105.  One request of 131071 keys (268 MB) takes 62 us: 53 for the keys
+// and 7 for the launch that joins its 512 parts.
 constexpr int kRowsD = 16;
 constexpr int kKeysD = 128;
 
@@ -968,8 +968,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
 // on a SIMD then use 55 % of its matrix unit.  An item's start and end, 23000
 // cycles where nothing overlaps, weigh as 6 tiles.  8192 tokens of 3 requests
 // behind up to 4096 cached ones (32 + 8 heads of 128, 519 GFLOP in visible pairs)
-// take 620 .. 655 us, 0.8 PFLOP/s, where a large bf16 matrix product reaches 1.42.
-// 8001 tokens with a window of 1000 (64 + 8 heads of 64, 132 GFLOP) take 318:
+// take 640 us, 0.8 PFLOP/s, where a large bf16 matrix product reaches 1.42.
+// 8001 tokens with a window of 1000 (64 + 8 heads of 64, 132 GFLOP) take 303:
 // tiles that the mask cuts are computed whole, and with D = 64 a key's softmax
 // stands beside half the products.
 //
