@@ -96,10 +96,12 @@ struct Request {
   int keys;            // keys that the table can hold and the length names
 };
 
-// keys of a request: key indices of its last tile stay below 2^31
+// keys of a request: key indices of the tiles that are read ahead of its last one,
+// at most 6 of 128 keys, stay below 2^31
+constexpr int kMostKeys = 0x7fff0000;
 __device__ __forceinline__ int keys_of(const AttentionArgs& a, int len, int32_t width) {
   int64_t cap = a.num_blocks > 0 ? (int64_t)width * a.page : 0;
-  cap = cap < 0x7fffff00ll ? cap : 0x7fffff00ll;
+  cap = cap < kMostKeys ? cap : kMostKeys;
   return len < 0 ? 0 : (int64_t)len < cap ? len : (int)cap;
 }
 

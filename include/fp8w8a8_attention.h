@@ -127,7 +127,8 @@ size_t fp8_attention_workspace_bytes(int shared_prefix, int64_t T, int64_t B, in
  * for the product with the values, not for the sum below it.
  * A query that sees no key (L = 0, p < 0, or only unmapped pages) gets zeros
  * and lse = -inf.  A key in a page that the table does not map (an entry
- * outside [0, num_blocks), or behind table_width) is not visible.  Codes in
+ * outside [0, num_blocks), or behind table_width) is not visible, nor is one
+ * at 2^31 - 65536 or behind it in its request or prefix.  Codes in
  * places that a query does not see, NaN among them, do not reach it.  Rows
  * of out and lse in no request's range are left as they were.  Offsets are
  * clamped to [0, T] and should be nondecreasing.

@@ -179,6 +179,28 @@ def test_widest_window():
     b.check(window=big, sinks=3)
 
 
+@pytest.mark.parametrize("n", [1, 70])
+def test_longest_requests(n):
+    """A request of 2^31 - 65536 keys in repeated blocks of 2^20, seen through a
+    window, against its last block alone; and a length that passes that."""
+    page, D, most = 1 << 20, 64, 0x7fff0000
+    rng = np.random.default_rng(n)
+    kc, vc = (torch.from_numpy(codes(rng, 2, page, 1, D)).cuda() for _ in range(2))
+    one = torch.ones(1, device="cuda")
+    q = bf16(synth.f32_to_bf16_bits((rng.standard_normal((n, 4, D)) * 0.15).astype(np.float32)))
+    table = np.zeros((1, 2048), dtype=np.int32)
+    table[0, 2047] = 1
+    offs = i32([0, n])
+    far = fp8.paged_attention(q, kc, vc, i32(table), i32([most]), offs, one, one, window=300)
+    near = fp8.paged_attention(q, kc, vc, i32([[1]]), i32([most - 2047 * page]), offs, one, one,
+                               window=300)
+    assert torch.isfinite(far.float()).all()
+    assert torch.equal(far.view(torch.int16), near.view(torch.int16))
+    out = fp8.paged_attention(q, kc, vc, i32(table), i32([(1 << 31) - 1]), offs, one, one,
+                              window=300)
+    assert (out == 0).all()                        # nothing of their windows is there
+
+
 def test_long_context():
     """One request over many shares, and a batch of more requests than a scan pass."""
     Batch(1, [(1, 20011)], 4, 1, 64).check()
