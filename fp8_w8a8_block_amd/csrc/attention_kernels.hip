@@ -823,8 +823,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, s[t][i]);
         top = max_xor32(max_xor16(top)) * c;
-        // the base moves where a row's maximum passes it by 2^8 (see the larger
-        // tiles below)
+        // the base moves where a row's maximum passes it by 2^8 (fp16 holds P up to
+        // 2^16 as exactly), so that O is rescaled a few times per item
         if (__ballot(top > m + 8.0f) != 0ull) {
           const float m_new = __builtin_fmaxf(m, top);
           const float alpha = __builtin_amdgcn_exp2f(m - base_of(m_new));
@@ -1761,7 +1761,8 @@ int compute_units() {
 // one request of all rows: of 32768 keys, 59 / 64 at 48 rows, 103 / 64 at 96.
 // D = 256 has the 16-row tiles only: 32 rows of O and Q fill a wave's registers
 // there, and 256-row tiles that spill took 1336 us where these take 199 (32
-// requests of 256 rows, 2048 keys).
+// requests of 256 rows, 2048 keys); two 16-row blocks per wave spilled too (202,
+// and 47 in place of 34 for 32 rows).
 bool many_rows(int64_t T, int64_t B, int64_t G, int64_t D) { return D < 256 && T * G > 48 * B; }
 
 struct Shape {
