@@ -3,16 +3,18 @@
 //
 // For a query row q at position p of its request (one row per query head):
 //   s_j = scale * k_scale * <q, dec(K_j)>,  out = v_scale * sum_j softmax(s)_j dec(V_j)
-// over the visible j.  One pass over the keys keeps a running maximum m, the
-// sum l = sum exp(s_j - m) and O = sum exp(s_j - m) V_j, rescaled when m grows.
+// over the visible j.  One pass over the keys keeps a base m near the running
+// maximum, the sum l = sum exp(s_j - m) and O = sum exp(s_j - m) V_j, rescaled
+// when m moves.
 //
 // Numbers.  E4M3 codes convert exactly to bf16 and to fp16 (4 significant
 // bits, 2^-9 .. 448), queries are bf16, so <q, K_j> is a sum of exact products
 // on the bf16 matrix instruction with fp32 accumulation, and nothing of the
-// scores is rounded below fp32.  P = exp(s - m) <= 2^8 goes to fp16, whose 11
-// bits keep its rounding (2^-11 relative, 2^-25 absolute below 2^-14) an order
-// under the bf16 output's; O is fp32, and l sums the fp32 values.  exp(x) is
-// exp2(x log2 e), the factor folded into the score scale.
+// scores is rounded below fp32.  P = exp(s - m) goes to fp16, 11 bits to the
+// bf16 output's 8; the base keeps a row's largest P at 2^10 .. 2^15, so that
+// weights down to 2^-24 of the largest have them all (see moved_base).  O is fp32,
+// and l sums the fp32 values.  exp(x) is exp2(x log2 e), the factor folded into
+// the score scale.
 //
 // Layout.  S^T = K Q^T puts one query row in each lane column, so m, l and the
 // rescaling of O^T = V^T P^T stay in the lane's own column, and P's registers
@@ -67,7 +69,7 @@ struct Split {
 // partial rows of a launch: workgroup w writes slot 2 w (an item that began
 // before its share) and slot 2 w + 1 (one that goes on behind it)
 struct Parts {
-  float* ml;           // [slots][R][2]: m (of the scores times log2 e) and l
+  float* ml;           // [slots][R][2]: base m (of the scores times log2 e) and l
   float* o;            // [slots][R][D]
   Split* split;        // [workgroups]
   // shared prefix only: where each row's result is, and rows that one
@@ -446,9 +448,22 @@ __device__ __forceinline__ float sum_xor16(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// the maximum that exponents are taken against: rows that have seen no key
-// (m = -inf) take 0, so that exp2(-inf - 0) = 0 and nothing turns NaN
+// what exponents are taken against: rows that have seen no key (m = -inf) take
+// 0, so that exp2(-inf - 0) = 0 and nothing turns NaN
 __device__ __forceinline__ float base_of(float m) { return m == FP8_NEG_INF ? 0.0f : m; }
+
+// The base m that a row's P = exp2(score - m), l and O are kept against.  It moves
+// where the row's maximum passes it by kReach, to kBelow under the maximum: the
+// largest P lies in 2^kBelow .. 2^kReach, fp16's upper end, and what is lost where
+// fp16 is subnormal, 2^-25, is 2^-35 of the largest weight.  Many small weights count
+// together: with m at the maximum (2^-25), 131071 keys 17.4 nats below an attention
+// sink, 0.0036 of the result, were all rounded to zero.  O is rescaled a few times
+// per item, as the maximum may grow by 2^5 before; 12 in place of 10 takes 306 us in
+// place of 302 for 8001 windowed tokens (64 + 8 heads of 64), 7 no less than 10.
+constexpr float kBelow = 10.0f, kReach = 15.0f;
+__device__ __forceinline__ float moved_base(float m, float top) {
+  return __builtin_fmaxf(m, top - kBelow);
+}
 
 // The keys that a row sees: lo .. hi and 0 .. sinks - 1 (up to hi).
 struct Sight {
@@ -823,10 +838,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, s[t][i]);
         top = max_xor32(max_xor16(top)) * c;
-        // the base moves where a row's maximum passes it by 2^8 (fp16 holds P up to
-        // 2^16 as exactly), so that O is rescaled a few times per item
-        if (__ballot(top > m + 8.0f) != 0ull) {
-          const float m_new = __builtin_fmaxf(m, top);
+        if (__ballot(top - m > kReach) != 0ull) {  // some row's maximum grew out of reach
+          const float m_new = moved_base(m, top);
           const float alpha = __builtin_amdgcn_exp2f(m - base_of(m_new));
           l *= alpha;
 #pragma unroll
@@ -959,10 +972,6 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
 // products j at 2 j + 2, those of the second group one interval later.  K j + 1
 // and V j are then read in 2 j + 2 and 2 j + 3; they were written in the two
 // intervals before, when their buffers' last readers were done.
-//
-// The exponents' base m moves only where a row's maximum passes it by 2^8 (P then
-// reaches 256, which fp16 holds as exactly as 1), so that O is rescaled a few
-// times per item and not in every other tile.
 //
 // Bound by the two phases' sum.  Measured at D = 128, per tile of 64 keys and wave:
 // products 1870 cycles (1024 of them the matrix unit's, the rest operands from LDS
@@ -1350,8 +1359,8 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
 #pragma unroll
             for (int v = 0; v < 16; ++v) top = __builtin_fmaxf(top, s[t][v]);
           top = max_xor32(top) * c;
-          if (__ballot(top > m + 8.0f) != 0ull) {  // some row's maximum grew out of reach
-            const float m_new = __builtin_fmaxf(m, top);
+          if (__ballot(top - m > kReach) != 0ull) {  // some row's maximum grew out of reach
+            const float m_new = moved_base(m, top);
             const float alpha = __builtin_amdgcn_exp2f(m - base_of(m_new));
             l *= alpha;
 #pragma unroll
@@ -1566,7 +1575,7 @@ __device__ __forceinline__ float wave_fmax(float x) {
   return x;
 }
 
-// maximum of the parts' m over a wave
+// largest of the parts' m over a wave
 __device__ __forceinline__ float parts_max(const float* ml, int64_t f, int np, int R) {
   float m = FP8_NEG_INF;
   for (int j = threadIdx.x & 63; j < np; j += 64)

@@ -96,7 +96,8 @@ def attention_ref(q, key_cache, value_cache, table, lens, offsets, scale, ks, vs
       scores: D exact products summed in fp32: D 2^-24 sum |q k| |c|, and two
               roundings (the scale factor, its product) of the score itself;
       exp2:   the difference's rounding and the instruction's 1 ulp, 2^-22;
-      P:      fp16, 2^-11 relative, 2^-25 absolute where it is subnormal;
+      P:      fp16, the row's largest at 2^10 or above: 2^-11 relative, 2^-35 of the
+              largest absolute where it is subnormal;
       sums:   fp32 over L terms and the joins of parts, (L + 64) 2^-24;
       result: bf16, 2^-8 relative.
     """
@@ -153,7 +154,7 @@ def attention_ref(q, key_cache, value_cache, table, lens, offsets, scale, ks, vs
                 absv = (w @ np.abs(v0)) / l1 * abs(vs)
                 rel = 2.0 ** -11 + 2 * ds + 2 * 2.0 ** -22 + 2 * sums
                 tol[a:e, g] = np.abs(np.where(np.isnan(o), 0, o)) * 2.0 ** -8 + absv * rel + \
-                    (vis @ np.abs(v0)) / l1 * abs(vs) * 2.0 ** -25
+                    (vis @ np.abs(v0)) / l1 * abs(vs) * 2.0 ** -35
                 tol_lse[a:e, g] = (ds + sums + 2.0 ** -22)[:, 0] + \
                     np.abs(np.where(np.isfinite(lse[a:e, g]), lse[a:e, g], 0)) * 2.0 ** -22
     return out, lse, tol, tol_lse, covered
