@@ -461,8 +461,19 @@ __device__ __forceinline__ float base_of(float m) { return m == FP8_NEG_INF ? 0.
 // per item, as the maximum may grow by 2^5 before; 12 in place of 10 takes 306 us in
 // place of 302 for 8001 windowed tokens (64 + 8 heads of 64), 7 no less than 10.
 constexpr float kBelow = 10.0f, kReach = 15.0f;
+// score - m is one fused operation, so that a score's product with its factor is
+// not rounded.  The maximum is: from 2^20 on it may differ from the exact product by
+// more than 2^-4, later by hundreds, and exp2 of that is no weight any more.  Where a
+// wave's base gets that large (of either sign), its tiles' scores are rounded to fp32
+// first, as the maximum is, and the base is the maximum itself.  A row whose base is
+// not has no weight from a score that is.  `reach` then sends every tile of the item
+// through the branch that moves the base, so that the others pay nothing for it.
+__device__ __forceinline__ bool huge(float x) {    // 2^20 < |x| < inf
+  constexpr uint32_t k = 0x49800001u;
+  return (__float_as_uint(x) & 0x7fffffffu) - k < 0x7f800000u - k;
+}
 __device__ __forceinline__ float moved_base(float m, float top) {
-  return __builtin_fmaxf(m, top - kBelow);
+  return __builtin_fmaxf(m, huge(top) ? top : top - kBelow);
 }
 
 // The keys that a row sees: lo .. hi and 0 .. sinks - 1 (up to hi).
@@ -741,6 +752,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
         qf[i] = load_query(p + 64 * (i / 2) + 8 * (i % 2), fac.flip);
     }
     float m = FP8_NEG_INF, l = 0.0f;
+    float base = 0.0f, reach = kReach;             // base: of m, what is subtracted
     f32x4 o[OT];
 #pragma unroll
     for (int j = 0; j < OT; ++j) o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -838,15 +850,24 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, s[t][i]);
         top = max_xor32(max_xor16(top)) * c;
-        if (__ballot(top - m > kReach) != 0ull) {  // some row's maximum grew out of reach
+        if (__ballot(top - m > reach) != 0ull) {  // some row's maximum grew out of reach
           const float m_new = moved_base(m, top);
           const float alpha = __builtin_amdgcn_exp2f(m - base_of(m_new));
           l *= alpha;
 #pragma unroll
           for (int j = 0; j < OT; ++j) o[j] *= alpha;
           m = m_new;
+          base = base_of(m);
+          if (__ballot(huge(m)) != 0ull) {         // see huge
+            reach = FP8_NEG_INF;
+            const float inv = 1.0f / c;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[t][i] = (s[t][i] * c - base) * inv;
+            base = 0.0f;
+          }
         }
-        const float base = base_of(m);
         float sum = 0.0f;
         f16x8 p;
 #pragma unroll
@@ -1081,6 +1102,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
     const int count = tl.count();
     const int kend = k1 < count ? k1 : count;
     float m, l;
+    float base, reach;                             // base: of m, what is subtracted
     f32x16 o[OB];
     NanBits<D / 64> nans;                          // of this lane's D / 2 values
 
@@ -1091,6 +1113,8 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
     for (bool careful = false;; careful = true) {
       m = FP8_NEG_INF;
       l = 0.0f;
+      base = 0.0f;
+      reach = kReach;
       nans = {};
 #pragma unroll
       for (int b = 0; b < OB; ++b)
@@ -1359,7 +1383,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
 #pragma unroll
             for (int v = 0; v < 16; ++v) top = __builtin_fmaxf(top, s[t][v]);
           top = max_xor32(top) * c;
-          if (__ballot(top - m > kReach) != 0ull) {  // some row's maximum grew out of reach
+          if (__ballot(top - m > reach) != 0ull) {  // some row's maximum grew out of reach
             const float m_new = moved_base(m, top);
             const float alpha = __builtin_amdgcn_exp2f(m - base_of(m_new));
             l *= alpha;
@@ -1368,8 +1392,19 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[b][i] *= alpha;
             m = m_new;
+            base = base_of(m);
+            if (__ballot(huge(m)) != 0ull) {       // see huge
+              reach = FP8_NEG_INF;
+              float d = c;
+              asm volatile("" : "+v"(d));          // its reciprocal is not kept through the loop
+              const float inv = 1.0f / d;
+#pragma unroll
+              for (int t = 0; t < NB; ++t)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) s[t][v] = (s[t][v] * c - base) * inv;
+              base = 0.0f;
+            }
           }
-          const float base = base_of(m);
           float sum = 0.0f;
           f16x8 p[KT / 16];
 #pragma unroll

@@ -125,7 +125,8 @@ size_t fp8_attention_workspace_bytes(int shared_prefix, int64_t T, int64_t B, in
  * The products <q, key> are exact with fp32 sums; scores, maxima, sums and
  * outputs are held in fp32; exp(s_j) is rounded to fp16 for the product with
  * the values, not for the sum below it: to 11 bits, and to a multiple of 2^-34
- * of the row's largest where it is below 2^-24 of that.
+ * of the row's largest where it is below 2^-24 of that.  Where the scores of a
+ * row pass 2^20 they are rounded to fp32 before the maximum is subtracted.
  * A query that sees no key (L = 0, p < 0, or only unmapped pages) gets zeros
  * and lse = -inf.  A key in a page that the table does not map (an entry
  * outside [0, num_blocks), or behind table_width) is not visible, nor is one
