@@ -1760,26 +1760,31 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
   }
 }
 
-// Shared prefix: a wave joins a row's parts of the prefix and of its request.
+// Shared prefix: a wave joins a row's parts of the prefix and of its request.  The
+// grid ends at kMostJoinBlocks (a dispatch holds fewer than 2^32 work-items), behind
+// which a wave takes several rows.
+constexpr int64_t kMostJoinBlocks = (int64_t)1 << 20;
+
 template <int D>
 __global__ __launch_bounds__(kThreads) void attention_prefix_join_kernel(AttentionArgs a, Parts p1,
                                                                          int R1, Parts p2,
                                                                          int R2) {
-  const int64_t flat = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (flat >= (int64_t)a.T * a.Hq) return;
-  const int2 w1 = p1.where[flat], w2 = p2.where[flat];
-  if (w2.y < 0) return;                            // a row of no request
-  const float v_scale = a.v_scale[0];
-  const float m1 = w1.y ? parts_max(p1.ml, w1.x, w1.y, R1) : p1.whole_ml[flat * 2];
-  const float m2 = w2.y ? parts_max(p2.ml, w2.x, w2.y, R2) : p2.whole_ml[flat * 2];
-  const float base = base_of(__builtin_fmaxf(m1, m2));
-  Sum<D> s = {};
-  if (w1.y) add_parts<D, 8>(s, p1.ml, p1.o, w1.x, w1.y, R1, base, 0, 1);
-  else add_row<D>(s, p1.whole_ml, p1.whole_o, flat, base);
-  if (w2.y) add_parts<D, 2>(s, p2.ml, p2.o, w2.x, w2.y, R2, base, 0, 1);
-  else add_row<D>(s, p2.whole_ml, p2.whole_o, flat, base);
-  const int64_t token = flat / a.Hq;
-  write_row<D>(a, s, base, v_scale, token, (int)(flat - token * a.Hq));
+  for (int64_t flat = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); flat < (int64_t)a.T * a.Hq;
+       flat += (int64_t)gridDim.x * 4) {
+    const int2 w1 = p1.where[flat], w2 = p2.where[flat];
+    if (w2.y < 0) continue;                        // a row of no request
+    const float v_scale = a.v_scale[0];
+    const float m1 = w1.y ? parts_max(p1.ml, w1.x, w1.y, R1) : p1.whole_ml[flat * 2];
+    const float m2 = w2.y ? parts_max(p2.ml, w2.x, w2.y, R2) : p2.whole_ml[flat * 2];
+    const float base = base_of(__builtin_fmaxf(m1, m2));
+    Sum<D> s = {};
+    if (w1.y) add_parts<D, 8>(s, p1.ml, p1.o, w1.x, w1.y, R1, base, 0, 1);
+    else add_row<D>(s, p1.whole_ml, p1.whole_o, flat, base);
+    if (w2.y) add_parts<D, 2>(s, p2.ml, p2.o, w2.x, w2.y, R2, base, 0, 1);
+    else add_row<D>(s, p2.whole_ml, p2.whole_o, flat, base);
+    const int64_t token = flat / a.Hq;
+    write_row<D>(a, s, base, v_scale, token, (int)(flat - token * a.Hq));
+  }
 }
 
 // ---- host ---------------------------------------------------------------------------
@@ -1886,8 +1891,9 @@ hipError_t launch_d(const AttentionArgs& a, hipStream_t st) {
   if (e != hipSuccess) return e;
   launch_main<D, false, true>(a, p2, s2, st);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(attention_prefix_join_kernel<D>, dim3((uint32_t)((rows + 3) / 4)),
-                     dim3(kThreads), 0, st, a, p1, s1.R, p2, s2.R);
+  const int64_t blocks = (rows + 3) / 4 < kMostJoinBlocks ? (rows + 3) / 4 : kMostJoinBlocks;
+  hipLaunchKernelGGL(attention_prefix_join_kernel<D>, dim3((uint32_t)blocks), dim3(kThreads), 0, st,
+                     a, p1, s1.R, p2, s2.R);
   return hipGetLastError();
 }
 

@@ -371,3 +371,34 @@ def test_refusals():
     with pytest.raises(TypeError):
         fp8.prefix_attention(q, kc, vc, i32([0]).long(), i32([1]), i32(b.table), i32(b.lens),
                              i32(b.offsets), one, one)
+
+
+def test_prefix_of_many_rows():
+    """More rows than waves of one grid: 2^26 and some, against slices of them.
+
+    Prefix and own keys are one key tile each, so that no share cuts a row's sums
+    and slices have the same bits."""
+    T, Hq, D, page, far, own, part = (1 << 21) + 1, 32, 64, 16, 40, 3, 1000
+    rng = np.random.default_rng(8)
+    kc, vc = (torch.from_numpy(codes(rng, 4, page, Hq, D)).cuda() for _ in range(2))
+    one = torch.ones(1, device="cuda")
+    q = torch.empty((T, Hq, D), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    for a in range(0, T, 1 << 17):
+        q[a:a + (1 << 17)] = torch.randn(q[a:a + (1 << 17)].shape, generator=g, device="cuda") * 0.15
+
+    def go(q, length):
+        lse = torch.full(q.shape[:2], 7.0, device="cuda")
+        out = torch.full_like(q, 7.0)
+        fp8.prefix_attention(q, kc, vc, i32([2, 0, 1]), i32([far]), i32([[3]]), i32([length]),
+                             i32([0, len(q)]), one, one, out=out, lse=lse)
+        return out, lse
+
+    out, lse = go(q, own)
+    edge = (1 << 26) // Hq
+    # the last three tokens are the ones that see own keys
+    for a in (0, edge // 16 - part // 2, edge // 3, edge - part - own, T - part):
+        o, l = go(q[a:a + part], own if a + part == T else 0)
+        assert torch.equal(out[a:a + part].view(torch.int16), o.view(torch.int16)), a
+        assert torch.equal(lse[a:a + part], l), a
+    assert torch.isfinite(lse).all() and not (lse == 7.0).any()
