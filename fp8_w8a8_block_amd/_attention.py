@@ -320,7 +320,12 @@ def prefix_attention(query, key_cache, value_cache, prefix_table, prefix_len, bl
     """paged_attention for requests that all start with the same prefix_len
     (int32 [1], on the device) tokens in the blocks prefix_table (int32):
     block_table and seq_lens describe what follows it in each request.  The
-    prefix's keys and values are read once for the whole batch."""
+    prefix's keys and values are read once for the whole batch.
+
+    Every query sees the whole prefix.  A request of n queries needs
+    seq_lens[r] >= n - 1 for that to be causal: with fewer own tokens its first
+    queries are tokens of the prefix, which paged_attention over the joined
+    tokens masks and this call does not."""
     if prefix_table is None or prefix_len is None:
         raise TypeError("prefix_table and prefix_len must be tensors")
     return _attention(query, key_cache, value_cache, (prefix_table, prefix_len), block_table,

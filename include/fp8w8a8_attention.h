@@ -157,11 +157,15 @@ fp8_status fp8_paged_attention(const uint16_t* query, int64_t ld_query, const ui
  *                block                                                     (input)
  *   block_table, seq_lens describe what follows the prefix in each request
  *   (token 0 of a request's own blocks is position prefix_len).
- * Every query sees the whole prefix and its own request's keys up to itself;
- * the result is that of fp8_paged_attention over the joined tokens, up to the
- * order of the fp32 sums.  The prefix is read once for groups of queries of
- * all requests together.  A negative prefix_len counts as 0; unmapped pages
- * of either table are not visible.  Rows in no request's range are left as
+ * Every query sees the whole prefix and its own request's keys up to itself.
+ * Where a request has seq_lens[r] >= n - 1 for its n queries, that is the
+ * result of fp8_paged_attention over the joined tokens, up to the order of
+ * the fp32 sums.  With fewer own tokens the first n - 1 - seq_lens[r] queries
+ * are tokens inside the prefix, and they see all of it nevertheless, also the
+ * keys behind themselves: to run a part of the prefix itself causally, call
+ * fp8_paged_attention over the joined tokens.  The prefix is read once for
+ * groups of queries of all requests together.  A negative prefix_len counts
+ * as 0; unmapped pages of either table are not visible.  Rows in no request's range are left as
  * they were.  workspace: fp8_attention_workspace_bytes(1, ...) bytes. */
 fp8_status fp8_prefix_attention(const uint16_t* query, int64_t ld_query, const uint8_t* key_cache,
                                 const uint8_t* value_cache, int64_t num_blocks, int64_t block_size,

@@ -402,3 +402,33 @@ def test_prefix_of_many_rows():
         assert torch.equal(out[a:a + part].view(torch.int16), o.view(torch.int16)), a
         assert torch.equal(lse[a:a + part], l), a
     assert torch.isfinite(lse).all() and not (lse == 7.0).any()
+
+
+@pytest.mark.parametrize("requests", [[(2, 1), (3, 2), (1, 0), (1, 4)],
+                                      [(60, 59), (70, 90), (1, 0), (90, 90)]])
+def test_prefix_equals_joined_requests_with_few_own_tokens(requests):
+    """All but one of a request's queries among its own tokens: still the joined form."""
+    far = 160
+    b = Batch(9, requests, 8, 2, 64, far=far)
+    b.check()
+    split = b.want(64 ** -0.5)
+    b.table = np.concatenate([b.far_row[None].repeat(len(requests), 0), b.table], 1)
+    b.lens, b.far = [n + far for n in b.lens], 0
+    b.check()
+    joined = b.want(64 ** -0.5)
+    for x, y in zip(split[:2], joined[:2]):          # one definition, in 64 bits
+        assert np.allclose(x, y, rtol=1e-12, atol=1e-12)
+
+
+@pytest.mark.parametrize("requests", [[(2, 0), (4, 1), (1, 1)], [(60, 20), (70, 3)]])
+def test_queries_inside_the_prefix_see_all_of_it(requests):
+    """Fewer own tokens than that: the first queries see what all others see of the prefix."""
+    b = Batch(10, requests, 8, 2, 64, far=100)
+    b.check()
+    out, lse = b.run()
+    b.lens = [0] * len(requests)                     # the prefix alone
+    o2, l2 = b.run()
+    for r, (n, length) in enumerate(requests):
+        first = slice(int(b.offsets[r]), int(b.offsets[r]) + n - length)
+        assert torch.equal(out[first].view(torch.int16), o2[first].view(torch.int16))
+        assert torch.equal(lse[first], l2[first])
