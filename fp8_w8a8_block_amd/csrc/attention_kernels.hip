@@ -1024,8 +1024,8 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
   constexpr int kThreads = kWaves * 64;
   constexpr int TK = kThreads / KT;                // threads of a key's row of K
   constexpr int TV = kThreads / (KT / 4);          // threads of four keys' rows of V
-  constexpr int KW = D / TK / 4;                   // dwords that one takes of the row of K,
-  constexpr int VW = D / TV / 4;                   // and of each of the rows of V
+  constexpr int KW = D / TK / 4;                   // dwords that one takes of the row of K
+  static_assert(D / TV == 4, "one of each of the rows of V");
   constexpr int kBuf = KT * D * 2;                 // bytes of a K or V buffer
   constexpr int kPieces = D / 8 < 16 ? D / 8 - 1 : 15;   // K's XOR range
   __shared__ __attribute__((aligned(16))) uint8_t s_kv[4 * kBuf];   // K0 K1 V0 V1
@@ -1050,15 +1050,14 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
   // K and of V; step i XORs 2 i.
   const uint32_t from_k = n * (2 * D) + (g ^ (n & kPieces)) * 16;
   const uint32_t from_v = 2 * kBuf + n * (2 * KT) + (g ^ ((n ^ (n >> 3)) & 7)) * 16;
-  // Writes: a thread puts 4 KW codes of key tid / TK, and of column e < 4 VW of
-  // its V columns half a piece, keys first_v .. + 3.  V row of column e: see the
-  // order of O^T's rows above; with first row r0 it is r0 + 32 (e / 16) +
-  // 8 (e / 4 % 4) + e % 4, and its piece's index XORs those too.
+  // Writes: a thread puts 4 KW codes of key tid / TK, and of each of its 4 V
+  // columns half a piece, keys first_v .. + 3.  Column e is V row r0 + e (see the
+  // order of O^T's rows above), whose pieces' index XORs e.
   const int key_k = tid / TK, x_v = tid % TV, y_v = tid / TV;
   const uint32_t to_k =
       key_k * (2 * D) + (((tid % TK) * (KW / 2)) ^ (key_k & kPieces)) * 16;
   const int first_v = (y_v >> 2) * 16 + ((y_v >> 1) & 1) * 4 + (y_v & 1) * 8;
-  const int rem_v = x_v * (4 * VW) % (D / 2);
+  const int rem_v = x_v * 4 % (D / 2);
   const int r0_v = (rem_v / 16) * 32 + ((rem_v / 4) % 4) * 8 + (x_v / (TV / 2)) * 4;
   const uint32_t to_v = 2 * kBuf + r0_v * (2 * KT) +
                         ((y_v >> 1) ^ ((r0_v ^ (r0_v >> 3)) & 7)) * 16 + (y_v & 1) * 8;
@@ -1098,7 +1097,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
         kPrefix ? args.a.prefix_table : args.a.table + (int64_t)at.r * a.ld_table;
     const uint8_t* vc = args.a.vc + (int64_t)at.h * D;
     const uint8_t* codes_k = args.a.kc + (int64_t)at.h * D + (tid % TK) * (4 * KW);   // this thread's
-    const uint8_t* codes_v = vc + x_v * (4 * VW);
+    const uint8_t* codes_v = vc + x_v * 4;
     const int count = tl.count();
     const int kend = k1 < count ? k1 : count;
     float m, l;
@@ -1120,7 +1119,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
       for (int b = 0; b < OB; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[b][i] = 0.0f;
-      uint32_t raw_k[KW], raw_v[4 * VW];
+      uint32_t raw_k[KW], raw_v[4];
       // The table's entry and the slot of key tid % KT of tile k.  The entry is
       // read without a branch (of the last key where there is none), so that
       // nothing waits for it before its use.
@@ -1147,15 +1146,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
       auto fetch_v = [&](int e, const int4& slots) {
         const int slot = e == 0 ? slots.x : e == 1 ? slots.y : e == 2 ? slots.z : slots.w;
         const uint8_t* p = codes_v + (uint64_t)(uint32_t)(slot < 0 ? 0 : slot) * stride;
-        if constexpr (VW == 1) {
-          raw_v[e] = *reinterpret_cast<const uint32_t*>(p);
-        } else {
-          const uint4 x = *reinterpret_cast<const uint4*>(p);
-          raw_v[4 * e] = x.x;
-          raw_v[4 * e + 1] = x.y;
-          raw_v[4 * e + 2] = x.z;
-          raw_v[4 * e + 3] = x.w;
-        }
+        raw_v[e] = *reinterpret_cast<const uint32_t*>(p);
       };
       auto slot_k = [&](int k) { return s_slot[k & 7][key_k]; };
       auto slots_v = [&](int k) {
@@ -1188,21 +1179,19 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
           const int4 sv = slots_v(k);
           const int s4[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int w = 0; w < VW; ++w) raw_v[e * VW + w] = s4[e] < 0 ? 0u : raw_v[e * VW + w];
+          for (int e = 0; e < 4; ++e) raw_v[e] = s4[e] < 0 ? 0u : raw_v[e];
         }
         if (careful) {
           uint32_t nan = 0u;
 #pragma unroll
-          for (int i = 0; i < 4 * VW; ++i) nan |= nan_codes(raw_v[i]);
+          for (int i = 0; i < 4; ++i) nan |= nan_codes(raw_v[i]);
           if (nan != 0u) s_nan[buf] = k;
 #pragma unroll
-          for (int i = 0; i < 4 * VW; ++i) raw_v[i] = without_nans(raw_v[i]);
+          for (int i = 0; i < 4; ++i) raw_v[i] = without_nans(raw_v[i]);
         }
       };
       // The codes in registers go to LDS, converted, in small steps u.
-      constexpr int kPutsK = 2 * KW, kPutsV = 10 * VW;
+      constexpr int kPutsK = 2 * KW, kPutsV = 10;
       uint32_t col[4], half_k[4], half[4];
       auto put_k = [&](int u, uint32_t to) {        // two codes; 16 bytes every 4 steps
         const int i = u / 4, j = u % 4;
@@ -1216,26 +1205,24 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
         }
       };
       auto put_v = [&](int u, uint32_t to) {        // a dword column of 4 keys in 10 steps
-        const int w = u / 10, j = u % 10;
-        if (j == 0) {
-          half[0] = __builtin_amdgcn_perm(raw_v[VW + w], raw_v[w], 0x05010400u);
-          half[1] = __builtin_amdgcn_perm(raw_v[VW + w], raw_v[w], 0x07030602u);
-          half[2] = __builtin_amdgcn_perm(raw_v[3 * VW + w], raw_v[2 * VW + w], 0x05010400u);
-          half[3] = __builtin_amdgcn_perm(raw_v[3 * VW + w], raw_v[2 * VW + w], 0x07030602u);
-        } else if (j == 1) {
+        if (u == 0) {
+          half[0] = __builtin_amdgcn_perm(raw_v[1], raw_v[0], 0x05010400u);
+          half[1] = __builtin_amdgcn_perm(raw_v[1], raw_v[0], 0x07030602u);
+          half[2] = __builtin_amdgcn_perm(raw_v[3], raw_v[2], 0x05010400u);
+          half[3] = __builtin_amdgcn_perm(raw_v[3], raw_v[2], 0x07030602u);
+        } else if (u == 1) {
           col[0] = __builtin_amdgcn_perm(half[2], half[0], 0x05040100u);
           col[1] = __builtin_amdgcn_perm(half[2], half[0], 0x07060302u);
           col[2] = __builtin_amdgcn_perm(half[3], half[1], 0x05040100u);
           col[3] = __builtin_amdgcn_perm(half[3], half[1], 0x07060302u);
-        } else if (j % 2 == 0) {
+        } else if (u % 2 == 0) {
           half[0] = __builtin_bit_cast(
-              uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(col[j / 2 - 1], 1.0f, false));
+              uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(col[u / 2 - 1], 1.0f, false));
         } else {
-          const int b = j / 2 - 1;                 // column e = 4 w + b
+          const int b = u / 2 - 1;                 // column
           half[1] = __builtin_bit_cast(
               uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(col[b], 1.0f, true));
-          const int flip = b ^ (w & 3) ^ ((w >> 2) * 4), down = (w >> 2) * 32 + (w & 3) * 8 + b;
-          *reinterpret_cast<uint2*>(s_kv + (to ^ (16 * flip)) + down * (2 * KT)) =
+          *reinterpret_cast<uint2*>(s_kv + (to ^ (16 * b)) + b * (2 * KT)) =
               make_uint2(half[0], half[1]);
         }
       };
@@ -1255,7 +1242,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
         // K k, K k + 1 and V k to LDS; K k + 2 and V k + 1 stay in registers
         int x[NB / 2];
         lane_slots(at.k, x);
-        uint32_t k0[KW], v0[4 * VW], k1[KW];
+        uint32_t k0[KW], v0[4], k1[KW];
         const auto load_k = [&](int k) {
           const int slot = slot_k(k);
 #pragma unroll
@@ -1271,17 +1258,17 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
         for (int i = 0; i < KW; ++i) k0[i] = raw_k[i];
         load_v(at.k);
 #pragma unroll
-        for (int i = 0; i < 4 * VW; ++i) v0[i] = raw_v[i];
+        for (int i = 0; i < 4; ++i) v0[i] = raw_v[i];
         load_k(at.k + 1);
 #pragma unroll
         for (int i = 0; i < KW; ++i) k1[i] = raw_k[i];
         load_k(at.k + 2);
         load_v(at.k + 1);
-        uint32_t k2[KW], v1[4 * VW];
+        uint32_t k2[KW], v1[4];
 #pragma unroll
         for (int i = 0; i < KW; ++i) k2[i] = raw_k[i], raw_k[i] = k0[i];
 #pragma unroll
-        for (int i = 0; i < 4 * VW; ++i) v1[i] = raw_v[i], raw_v[i] = v0[i];
+        for (int i = 0; i < 4; ++i) v1[i] = raw_v[i], raw_v[i] = v0[i];
 #pragma unroll
         for (int u = 0; u < kPutsK; ++u) put_k(u, to_k);
         mend_v(at.k, 0, any_gap(x));
@@ -1294,7 +1281,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void attention_tile_kernel(Kern
 #pragma unroll
         for (int i = 0; i < KW; ++i) raw_k[i] = k2[i];
 #pragma unroll
-        for (int i = 0; i < 4 * VW; ++i) raw_v[i] = v1[i];
+        for (int i = 0; i < 4; ++i) raw_v[i] = v1[i];
         __syncthreads();
         if (second) __syncthreads();               // half a period behind
         // S^T: block t holds keys 32 t + 8 (v / 4) + 4 g + v % 4 of row n
