@@ -432,3 +432,16 @@ def test_queries_inside_the_prefix_see_all_of_it(requests):
         first = slice(int(b.offsets[r]), int(b.offsets[r]) + n - length)
         assert torch.equal(out[first].view(torch.int16), o2[first].view(torch.int16))
         assert torch.equal(lse[first], l2[first])
+
+
+@pytest.mark.parametrize("heads,D", [((4, 1), 64), ((8, 2), 128)])
+def test_more_requests_than_a_scan_pass_of_the_large_tiles(heads, D):
+    """Requests behind the 512th and the 1024th of the 256-row kernel's shares, some
+    without queries or keys; one of several row tiles behind them."""
+    rng = np.random.default_rng(D)
+    many = [(int(n), int(max(0, n + s))) for n, s in
+            zip(rng.integers(0, 40, 1100), rng.integers(-20, 60, 1100))]
+    many[1030] = (300, 700)
+    assert sum(n for n, _ in many) * heads[0] // heads[1] > 48 * len(many)
+    Batch(D, many, *heads, D, pad=5).check()
+    Batch(D + 1, many[:700], *heads, D, far=150).check()

@@ -77,3 +77,33 @@ def test_one_key_wins(power, D, requests, below):
                 # below half a step of a value of 4 bits, which comes out exact
                 assert np.array_equal(out[offsets[r] + i, h], vd[seen[best], h // 2] * vs), (r, i, h)
     assert clear > 0.75 * T * Hq
+
+
+@pytest.mark.parametrize("n", [1, 60])                 # tokens per request: either kernel
+@pytest.mark.parametrize("power", [22, 29, 90])
+def test_one_key_wins_behind_a_prefix(n, power):
+    """Head 0's largest score is in the shared prefix, head 1's among a request's own keys."""
+    rng = np.random.default_rng([n, power])
+    B, D, page, far, own = 5, 64, 16, 333, 77
+    shared, mine = -(-far // page), -(-own // page)
+    kc = np.zeros((shared + mine, page, 2, D), dtype=np.uint8)
+    kc[..., 0] = 0x38                                  # 1, but 16 at the two that win
+    vc = rng.integers(0x20, 0x58, kc.shape, dtype=np.uint8)
+    kc[200 // page, 200 % page, 0, 0] = kc[shared, 5, 1, 0] = 0x58
+    q = torch.zeros((B * n, 2, D), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 2.0 ** power
+
+    def i32(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    lse = torch.empty((B * n, 2), device="cuda")
+    out = fp8.prefix_attention(
+        q, torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), i32(list(range(shared))),
+        i32([far]), i32([list(range(shared, shared + mine))] * B), i32([own] * B),
+        i32(list(range(0, B * n + 1, n))), torch.ones(1, device="cuda"),
+        torch.ones(1, device="cuda"), scale=0.3, lse=lse).float().cpu()
+    for h, at in ((0, (200 // page, 200 % page, 0)), (1, (shared, 5, 1))):
+        want = torch.from_numpy(e4m3.decode(vc[at]).astype(np.float32))
+        assert torch.equal(out[:, h], want.expand(B * n, D)), h
+    top = float(np.float32(0.3)) * 16 * 2.0 ** power
+    assert torch.allclose(lse.cpu().double(), torch.tensor(top, dtype=torch.float64), rtol=2.0 ** -21)
