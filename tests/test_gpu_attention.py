@@ -445,3 +445,22 @@ def test_more_requests_than_a_scan_pass_of_the_large_tiles(heads, D):
     assert sum(n for n, _ in many) * heads[0] // heads[1] > 48 * len(many)
     Batch(D, many, *heads, D, pad=5).check()
     Batch(D + 1, many[:700], *heads, D, far=150).check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("shared", [False, True])
+def test_one_workspace_serves_any_number_of_requests(D, shared):
+    """Sized for all tokens in one request, it is large enough for fewer and for any batch."""
+    def need(T, B):
+        return fp8.attention_workspace_bytes(T, B, 8, 2, D, shared_prefix=shared)
+
+    sizes = [1, 3, 12, 13, 64, 500, 4000]
+    for T in sizes:
+        for B in (1, 2, 5, 40, 400):
+            assert need(T, B) <= need(T, 1), (T, B)
+            assert all(need(t, B) <= need(T, B) for t in sizes if t <= T), (T, B)
+    ws = torch.empty(need(600, 1), dtype=torch.uint8, device="cuda")
+    for requests in ([(1, 40)] * 50, [(300, 300), (2, 9)]):
+        b = Batch(D, requests, 8, 2, D, far=70 if shared else 0)
+        out, lse = b.run(workspace=ws)
+        close(f64(out), lse.cpu().numpy().astype(np.float64), b.want(D ** -0.5))
