@@ -29,9 +29,11 @@
 // key tiles its mask leaves.  A fixed grid of workgroups takes even shares of
 // the whole list's tiles, found by a prefix sum over the requests that every
 // workgroup forms itself, so no length is needed on the host and ragged
-// batches, one long context and many short ones all fill the card.  An item
-// inside one share is finished there; one that shares cut leaves fp32 partial
-// rows (O, m, l) in the workspace, and a second launch joins them.
+// batches, one long context and many short ones all fill the card.  Items of a
+// few tiles, a prompt's first ones, take longer than their tiles say: their start
+// and end are not counted.  An item inside one share is finished there; one that
+// shares cut leaves fp32 partial rows (O, m, l) in the workspace, and a second
+// launch joins them.
 #include <atomic>
 
 #include "attention_launch.h"
@@ -994,16 +996,17 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attention_rows_ker
 // and V j are then read in 2 j + 2 and 2 j + 3; they were written in the two
 // intervals before, when their buffers' last readers were done.
 //
-// Bound by the two phases' sum.  Measured at D = 128, per tile of 64 keys and wave:
-// products 1870 cycles (1024 of them the matrix unit's, the rest operands from LDS
-// and the staging in between), softmax 1430, waits at the barriers 430; two waves
-// on a SIMD then use 55 % of its matrix unit.  An item's start and end, 23000
-// cycles where nothing overlaps, weigh as 6 tiles.  8192 tokens of 3 requests
-// behind up to 4096 cached ones (32 + 8 heads of 128, 519 GFLOP in visible pairs)
-// take 640 us, 0.8 PFLOP/s, where a large bf16 matrix product reaches 1.42.
-// 8001 tokens with a window of 1000 (64 + 8 heads of 64, 132 GFLOP) take 303:
-// tiles that the mask cuts are computed whole, and with D = 64 a key's softmax
-// stands beside half the products.
+// Bound by the longer phase, twice per tile, as the groups are half a period apart.
+// Measured at D = 128, per tile of 64 keys and wave: products 1880 cycles (1024 of
+// them the matrix unit's, the rest operands from LDS and the staging in between),
+// softmax 1390 and 450 of waiting for the other group's products; two waves on a
+// SIMD then use 55 % of its matrix unit.  At D = 64, per tile of 128 keys, softmax
+// is the longer one, 2550 to 1950.  An item's start and end, 25000 cycles where
+// nothing overlaps, weigh as 6 to 7 tiles.  8192 tokens of 3 requests behind up to
+// 4096 cached ones (32 + 8 heads of 128, 519 GFLOP in visible pairs) take 616 to
+// 670 us, 0.8 PFLOP/s, where a large bf16 matrix product reaches 1.42.  8001 tokens
+// with a window of 1000 (64 + 8 heads of 64, 132 GFLOP) take 306: tiles that the
+// mask cuts are computed whole, and a key's softmax stands beside half the products.
 //
 // LDS rows are cut into 16-byte pieces whose index is XORed with the row's, so
 // that the 32 rows that one read names lie in different banks.  O^T's rows
@@ -1790,7 +1793,8 @@ int compute_units() {
 }
 
 // Whether B requests' T query tokens take the 256-row tiles: from 48 rows per
-// request on average.  Measured (us, 16-row against 256-row tiles): 64 requests
+// request on average, as the host does not know their lengths.  Measured on batches
+// of one kind (us, 16-row against 256-row tiles): 64 requests
 // of 2048 keys, D = 128, Hk = 8: 64 / 147 at 16 rows, 110 / 143 at 32, 151 / 144
 // at 48, 199 / 142 at 64; 4 requests of 16000: 73 / 92 at 32, 108 / 105 at 64;
 // 32 requests of 2048, D = 64: 38 / 50 at 32, 69 / 52 at 64.  A shared prefix is

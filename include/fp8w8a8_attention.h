@@ -101,7 +101,8 @@ fp8_status fp8_qk_norm_rope_cache(const uint16_t* query, int64_t ld_query, const
 
 /* Bytes of workspace that fp8_paged_attention (shared_prefix = 0) or
  * fp8_prefix_attention (nonzero) needs for T query tokens in B requests on
- * the current device. */
+ * the current device.  It grows with T and may shrink as B grows: what (T, 1)
+ * needs is enough for T tokens in any number of requests. */
 size_t fp8_attention_workspace_bytes(int shared_prefix, int64_t T, int64_t B, int64_t Hq,
                                      int64_t Hk, int64_t D);
 
@@ -135,8 +136,8 @@ size_t fp8_attention_workspace_bytes(int shared_prefix, int64_t T, int64_t B, in
  * of out and lse in no request's range are left as they were.  Offsets are
  * clamped to [0, T] and should be nondecreasing.
  * D 64, 128 or 256; Hq a multiple of Hk; window, sinks >= 0 (sinks without a
- * window change nothing); num_blocks * block_size < 2^31; a request's
- * T * Hq / Hk < 2^31.  The result does not depend on timing.
+ * window change nothing); num_blocks * block_size < 2^31; T * Hq < 2^31.  The
+ * result does not depend on timing.
  * workspace: fp8_attention_workspace_bytes(0, T, B, Hq, Hk, D) bytes, 16-byte
  * aligned, contents not needed and not read afterwards; calls that can
  * overlap need one each. */
