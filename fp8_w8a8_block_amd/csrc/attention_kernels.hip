@@ -460,8 +460,8 @@ __device__ __forceinline__ float base_of(float m) { return m == FP8_NEG_INF ? 0.
 // fp16 is subnormal, 2^-25, is 2^-35 of the largest weight.  Many small weights count
 // together: with m at the maximum (2^-25), 131071 keys 17.4 nats below an attention
 // sink, 0.0036 of the result, were all rounded to zero.  O is rescaled a few times
-// per item, as the maximum may grow by 2^5 before; 12 in place of 10 takes 306 us in
-// place of 302 for 8001 windowed tokens (64 + 8 heads of 64), 7 no less than 10.
+// per item, as the maximum may grow by 2^5 before; 12 in place of 10 takes 1.3 %
+// longer for 8001 windowed tokens (64 + 8 heads of 64), 7 no less time than 10.
 constexpr float kBelow = 10.0f, kReach = 15.0f;
 // score - m is one fused operation, so that a score's product with its factor is
 // not rounded.  The maximum is: from 2^20 on it may differ from the exact product by
@@ -1794,11 +1794,11 @@ int compute_units() {
 
 // Whether B requests' T query tokens take the 256-row tiles: from 48 rows per
 // request on average, as the host does not know their lengths.  Measured on batches
-// of one kind (us, 16-row against 256-row tiles): 64 requests
-// of 2048 keys, D = 128, Hk = 8: 64 / 147 at 16 rows, 110 / 143 at 32, 151 / 144
-// at 48, 199 / 142 at 64; 4 requests of 16000: 73 / 92 at 32, 108 / 105 at 64;
-// 32 requests of 2048, D = 64: 38 / 50 at 32, 69 / 52 at 64.  A shared prefix is
-// one request of all rows: of 32768 keys, 59 / 64 at 48 rows, 103 / 64 at 96.
+// of one kind (us, 16-row against 256-row tiles): 64 requests of 2048 keys, D = 128,
+// Hk = 8: 64 / 147 at 16 rows, 110 / 143 at 32, 151 / 144 at 48, 199 / 142 at 64; 4
+// requests of 16000: 73 / 92 at 32, 108 / 105 at 64; 32 requests of 2048, D = 64:
+// 38 / 50 at 32, 69 / 52 at 64.  A shared prefix is one request of all rows: of 32768
+// keys, 59 / 64 at 48 rows, 103 / 64 at 96.
 // D = 256 has the 16-row tiles only: 32 rows of O and Q fill a wave's registers
 // there, and 256-row tiles that spill took 1336 us where these take 199 (32
 // requests of 256 rows, 2048 keys); two 16-row blocks per wave spilled too (202,
