@@ -23,7 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8w8a8.so")
 SOURCES = ["abi.hip", "quant_kernels.hip", "gemm_kernels.hip", "kv_kernels.hip",
-           "attention_abi.hip", "slot_kernels.hip", "rope_kernels.hip", "attention_kernels.hip"]
+           "attention_abi.hip", "slot_kernels.hip", "rope_kernels.hip", "attention_kernels.hip",
+           "step_abi.hip", "norm_kernels.hip", "int4_kernels.hip", "logprob_kernels.hip"]
 PROBE_SOURCE = "hbm_probe.hip"                 # bench.py's HBM and matrix-unit references
 PROBE_LIB = os.path.join(PKG, "libhbmprobe.so")
 ARGS_SOURCE = "tensor_args.cpp"                # the binding's reader of tensor arguments

@@ -230,4 +230,49 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
   return u >> 16;
 }
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// ---- values computed in fp32 ----------------------------------------------
+// two fp32 to bf16, round to nearest even, in one instruction
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+// 1 / sqrt(x), x >= 0, within 1 ulp; the instruction does not take subnormals
+__device__ __forceinline__ float rsqrt_of(float x) {
+  const bool tiny = x < 0x1p-100f;
+  const float r = __builtin_amdgcn_rsqf(tiny ? x * 0x1p+100f : x);
+  return tiny ? r * 0x1p+50f : r;
+}
+
+// E4M3 codes of 8 fp32 values divided by a static scale.  The quotient takes
+// the steps of quant8_static; for an fp32 dividend it may be off by one ulp of
+// fp32 (a bf16 one is exact), 2^-19 of an E4M3 step.
+__device__ __forceinline__ uint2 quant8_f32(const float z[8], const StaticDivisor& d) {
+  bool direct = !d.fast;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) direct |= z[e] != z[e];
+  uint32_t o[2] = {0u, 0u};
+  if (direct) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      o[e / 4] |= (uint32_t)e4m3_encode_one(z[e] / d.s) << (8 * (e & 3));
+    return make_uint2(o[0], o[1]);
+  }
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // s' is below 2, so what is cut here has a quotient beyond 448
+    const float x = __builtin_ldexpf(z[e], d.k);
+    const float xa = __builtin_amdgcn_fmed3f(x, -1024.0f, 1024.0f);
+    const float q0 = xa * d.r;
+    const float r = __builtin_fmaf(-q0, d.sp, xa);
+    q[e] = __builtin_amdgcn_fmed3f(__builtin_fmaf(r, d.r, q0), -kE4M3Max, kE4M3Max);
+  }
+  o[0] = e4m3_pack4_mag(q[0], q[1], q[2], q[3]) ^ d.sign;
+  o[1] = e4m3_pack4_mag(q[4], q[5], q[6], q[7]) ^ d.sign;
+  return make_uint2(o[0], o[1]);
+}
+
 }  // namespace fp8k

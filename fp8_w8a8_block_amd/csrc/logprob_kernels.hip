@@ -1,0 +1,560 @@
+// Log probabilities of given tokens, with rank, entropy and the k most likely
+// alternatives, for gfx950.
+//
+// With t = (x - m) c, c = scale log2(e), m the row's maximum, over one pass:
+//   S = sum 2^t,  D = sum t 2^t,
+//   log p = scale (x_token - m) - ln2 log2 S,  entropy = ln2 (log2 S - D / S),
+// S and D rescaled when the running maximum grows.  x - m is formed first, so
+// that nothing is lost at large logits or a mask of the type's lowest value.
+//
+// The alternatives need no second pass over the row.  It is seen as segments of
+// 128 bytes, whose maxima are kept (the softmax needs them anyway).  512 threads
+// hold the maximum of a run of segments each; the k-th largest of these bounds
+// the k-th largest logit from below, so only the segments that reach it are read
+// again, and of them only the logits that reach it are ranked.
+#include <type_traits>
+
+#include "device_common.h"
+#include "fp8w8a8_step.h"
+#include "launch.h"
+#include "step_launch.h"
+
+namespace fp8k {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kSweep = kThreads / 8;         // segments that the workgroup reads at once
+constexpr int kMaxSegments = 4096;           // kept in LDS by the one-launch form
+constexpr int kMaxListed = 192;              // segments read again
+constexpr int kMaxRanked = 512;              // logits ranked
+
+constexpr float kInf = __builtin_huge_valf();
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLog2e = 1.44269504088896341f;
+
+// maximum, S, D and the number of logits above the token's, of a part of a row
+struct Stats {
+  float m, s, d;
+  uint32_t above;
+};
+
+__device__ __forceinline__ float anchor(float m) { return m == -kInf ? 0.0f : m; }
+
+// (s, d) relative to the maximum m, moved to the maximum to >= m.  A NaN in s or d
+// stays one, so nothing here may be 0 times infinity, nor drop a factor of 0.
+__device__ __forceinline__ void rebase(float m, float to, float c, float& s, float& d) {
+  const float by = m == -kInf ? 0.0f : __builtin_fmaxf((m - to) * c, -1000.0f);
+  const float f = __builtin_amdgcn_exp2f(by);
+  d = f * __builtin_fmaf(s, by, d);
+  s = f * s;
+}
+
+__device__ __forceinline__ void join(Stats& a, float m, float s, float d, float c) {
+  const float to = __builtin_fmaxf(a.m, m);
+  rebase(a.m, to, c, a.s, a.d);
+  rebase(m, to, c, s, d);
+  a.m = to;
+  a.s += s;
+  a.d += d;
+}
+
+// A row as vectors of 16 bytes from the 128-byte line on in which it starts:
+// vector v, value e is logit v V + e - lead.
+template <bool kF32>
+struct Row {
+  static constexpr int V = kF32 ? 4 : 8;
+  const uint4* base;
+  uint32_t lead, n;            // n logits
+
+  __device__ __forceinline__ Row(const void* logits, int64_t ld, int64_t row, int64_t vocab) {
+    const uintptr_t p = (uintptr_t)logits + (uintptr_t)(row * ld) * (kF32 ? 4 : 2);
+    base = reinterpret_cast<const uint4*>(p & ~(uintptr_t)127);
+    lead = (uint32_t)((p & 127) / (kF32 ? 4 : 2));
+    n = (uint32_t)vocab;
+  }
+  __device__ __forceinline__ bool whole(uint32_t v) const {
+    return v * V >= lead && v * V + V <= lead + n;
+  }
+  __device__ __forceinline__ static void unpack(const uint4 r, float x[V]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      x[e] = kF32 ? __uint_as_float(w[e]) : (e & 1) ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+  }
+  // logit i < n
+  __device__ __forceinline__ float at(uint32_t i) const {
+    if (kF32) return reinterpret_cast<const float*>(base)[lead + i];
+    return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[lead + i] << 16);
+  }
+  // any vector: -inf where there is no logit; `fits` has a bit for each that is one
+  __device__ __forceinline__ uint32_t load(uint32_t v, float x[V]) const {
+    if (whole(v)) {
+      unpack(base[v], x);
+      return (1u << V) - 1u;
+    }
+    uint32_t fits = 0u;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const uint32_t i = v * V + e - lead;          // wraps in front of the row
+      x[e] = -kInf;
+      if (i < n) {
+        x[e] = at(i);
+        fits |= 1u << e;
+      }
+    }
+    return fits;
+  }
+};
+
+// maximum over the 8 lanes that hold a segment
+__device__ __forceinline__ float segment_max(float v) {
+  auto other = [](float x, auto ctrl) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+        0, (int)__float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  v = __builtin_fmaxf(v, other(v, std::integral_constant<int, 0xb1>()));    // lane ^ 1
+  v = __builtin_fmaxf(v, other(v, std::integral_constant<int, 0x4e>()));    // lane ^ 2
+  return __builtin_fmaxf(v, other(v, std::integral_constant<int, 0x141>())); // 7 - lane of 8
+}
+
+// One batch of U vectors a thread, kThreads apart: x is theirs.
+template <bool kF32, int U>
+__device__ __forceinline__ void take(const float (&x)[U][Row<kF32>::V], float c, float mine,
+                                     Stats& a, float* maxima) {
+  constexpr int V = Row<kF32>::V;
+  float top[U], m = a.m;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    top[u] = x[u][0];
+#pragma unroll
+    for (int e = 1; e < V; ++e) top[u] = __builtin_fmaxf(top[u], x[u][e]);
+    m = __builtin_fmaxf(m, top[u]);
+  }
+  rebase(a.m, m, c, a.s, a.d);
+  a.m = m;
+  const float from = anchor(m);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float t = (x[u][e] - from) * c, w = __builtin_amdgcn_exp2f(t);
+      a.s += w;
+      // a weight of 0 has an exponent of -inf, and no part in D
+      a.d = __builtin_fmaf(w, __builtin_fmaxf(t, -1000.0f), a.d);
+      a.above += (uint32_t)__builtin_popcountll(__ballot(x[u][e] > mine));
+    }
+    const float seg = segment_max(top[u]);
+    if ((threadIdx.x & 7u) == 0) maxima[u * kSweep + (threadIdx.x >> 3)] = seg;
+  }
+}
+
+// Segments first .. last - 1 of a row, their maxima to maxima[0 ..]; the sums of
+// the whole workgroup in every thread.
+template <bool kF32>
+__device__ Stats stream(const Row<kF32>& row, uint32_t first, uint32_t last, float c, float mine,
+                        float* maxima) {
+  constexpr int V = Row<kF32>::V, U = 4;
+  __shared__ Stats shared[kThreads / 64];
+  Stats a = {-kInf, 0.0f, 0.0f, 0u};
+  uint32_t seg = first;
+  while (seg < last) {
+    const uint32_t v = seg * 8u + threadIdx.x;
+    // all of the batch inside the row, for all threads alike
+    if (seg + U * kSweep <= last && row.whole(seg * 8u) &&
+        row.whole((seg + U * kSweep) * 8u - 1u)) {
+      uint4 r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) r[u] = row.base[v + u * kThreads];
+      float x[U][V];
+#pragma unroll
+      for (int u = 0; u < U; ++u) row.unpack(r[u], x[u]);
+      take<kF32, U>(x, c, mine, a, maxima + (seg - first));
+      seg += U * kSweep;
+    } else {
+      // one vector a thread; behind the last segment there is nothing to take
+      float x[1][V];
+      if (seg + (threadIdx.x >> 3) < last) {
+        row.load(v, x[0]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[0][e] = -kInf;
+      }
+      take<kF32, 1>(x, c, mine, a, maxima + (seg - first));
+      seg += kSweep;
+    }
+  }
+  for (int i = 1; i < 64; i <<= 1)
+    join(a, __shfl_xor(a.m, i), __shfl_xor(a.s, i), __shfl_xor(a.d, i), c);
+  if ((threadIdx.x & 63u) == 0) shared[threadIdx.x >> 6] = a;
+  __syncthreads();
+  Stats all = shared[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 64; ++w) {
+    join(all, shared[w].m, shared[w].s, shared[w].d, c);
+    all.above += shared[w].above;
+  }
+  return all;
+}
+
+// fp32 bits in the values' order
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x == 0.0f ? 0.0f : x);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+struct Select {
+  float super[kThreads];
+  uint32_t listed[kMaxListed];
+  float value[kMaxRanked];
+  uint32_t index[kMaxRanked];
+  uint32_t hist[256];
+  uint32_t wave[kThreads / 64];
+  uint32_t segments, ranked, bin, left;
+  float bound;
+};
+
+// Largest key that at least k of the 512 values reach (or a key between it and
+// the next lower one that exactly k reach); one wave, k <= 512.
+__device__ __forceinline__ uint32_t kth_key(const float* v, uint32_t k) {
+  uint32_t key[kThreads / 64], found = 0u;
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) key[i] = order_key(v[i * 64 + (threadIdx.x & 63u)]);
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t t = found | (1u << bit);
+    uint32_t n = 0u;
+#pragma unroll
+    for (int i = 0; i < kThreads / 64; ++i)
+      n += (uint32_t)__builtin_popcountll(__ballot(key[i] >= t));
+    if (n >= k) found = t;
+    if (n == k) break;
+  }
+  return found;
+}
+
+// f(value, index) for every logit of the row, in any order
+template <bool kF32, typename F>
+__device__ __forceinline__ void each_logit(const Row<kF32>& row, F f) {
+  constexpr int V = Row<kF32>::V;
+  const uint32_t vectors = (row.lead + row.n + V - 1) / V;
+  for (uint32_t v = threadIdx.x; v < vectors; v += kThreads) {
+    float x[V];
+    const uint32_t fits = row.load(v, x);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (fits >> e & 1u) f(x[e], v * V + e - row.lead);
+  }
+}
+
+// The k most likely logits of a row, by falling value and rising index.  `log_p`
+// turns a logit into what is written.
+template <bool kF32, typename F>
+__device__ void select_top(const Row<kF32>& row, const float* maxima, uint32_t segments, uint32_t k,
+                           float* top, int32_t* ids, Select& sh, F log_p) {
+  constexpr int V = Row<kF32>::V;
+  const uint32_t tid = threadIdx.x;
+  const uint32_t per = (segments + kThreads - 1) / kThreads;
+  const uint32_t s0 = tid * per, s1 = s0 + per < segments ? s0 + per : segments;
+  float m = -kInf;
+  for (uint32_t s = s0; s < s1; ++s) m = __builtin_fmaxf(m, maxima[s]);
+  sh.super[tid] = m;
+  if (tid == 0) sh.segments = sh.ranked = 0u;
+  __syncthreads();
+  if (tid < 64) {
+    const uint32_t key = kth_key(sh.super, k);
+    if (tid == 0) {
+      const float f = __uint_as_float(key ^ (key & 0x80000000u ? 0x80000000u : 0xffffffffu));
+      sh.bound = f == f ? f : -kInf;                // below -inf in the order: no bound
+    }
+  }
+  __syncthreads();
+  const float bound = sh.bound;
+  // masked logits are not listed: the lowest of them are filled in below
+  auto passes = [&](float x) { return x >= bound && x > -kInf; };
+  if (passes(m))
+    for (uint32_t s = s0; s < s1; ++s)
+      if (passes(maxima[s])) {
+        const uint32_t i = atomicAdd(&sh.segments, 1u);
+        if (i < kMaxListed) sh.listed[i] = s;
+      }
+  __syncthreads();
+  const uint32_t listed = sh.segments;
+  auto rank_this = [&](float x, uint32_t index) {
+    const uint32_t i = atomicAdd(&sh.ranked, 1u);
+    if (i < kMaxRanked) {
+      sh.value[i] = x;
+      sh.index[i] = index;
+    }
+  };
+  if (listed <= kMaxListed) {
+    for (uint32_t i = tid >> 3; i < listed; i += kSweep) {
+      const uint32_t v = sh.listed[i] * 8u + (tid & 7u);
+      float x[V];
+      const uint32_t fits = row.load(v, x);
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if ((fits >> e & 1u) && passes(x[e])) rank_this(x[e], v * V + e - row.lead);
+    }
+  }
+  __syncthreads();
+  uint32_t ranked = sh.ranked, equal = order_key(-kInf);
+  if (listed > kMaxListed || ranked > kMaxRanked) {
+    // Many equal logits, or many large ones in a few segments: the k-th largest
+    // key is found digit by digit over the whole row; what is larger is ranked,
+    // and the first of its equals are filled in.
+    uint32_t prefix = 0u, left = k;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      __syncthreads();
+      if (tid < 256) sh.hist[tid] = 0u;
+      __syncthreads();
+      each_logit(row, [&](float x, uint32_t) {
+        const uint32_t key = order_key(x);
+        if (shift < 24 && (key >> (shift + 8)) != (prefix >> (shift + 8))) return;
+        // lanes of the first one's digit count together
+        const uint32_t bin = key >> shift & 255u, lead_bin = __builtin_amdgcn_readfirstlane(bin);
+        const uint64_t same = __ballot(bin == lead_bin);
+        if (bin != lead_bin)
+          atomicAdd(&sh.hist[bin], 1u);
+        else if ((tid & 63u) == (uint32_t)__builtin_ctzll(same))
+          atomicAdd(&sh.hist[bin], (uint32_t)__builtin_popcountll(same));
+      });
+      __syncthreads();
+      if (tid < 64) {
+        // lane l: digits 255 - 4 l .. 252 - 4 l
+        uint32_t h[4], sum = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += h[i] = sh.hist[255u - 4u * tid - i];
+        uint32_t before = sum;
+        for (int i = 1; i < 64; i <<= 1) {
+          const uint32_t o = __shfl_up(before, i);
+          if ((int)tid >= i) before += o;
+        }
+        before -= sum;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (before < left && left <= before + h[i]) {
+            sh.bin = 255u - 4u * tid - i;
+            sh.left = left - before;
+          }
+          before += h[i];
+        }
+      }
+      __syncthreads();
+      prefix |= sh.bin << shift;
+      left = sh.left;
+    }
+    equal = prefix;
+    if (tid == 0) sh.ranked = 0u;
+    __syncthreads();
+    each_logit(row, [&](float x, uint32_t index) {
+      if (order_key(x) > equal) rank_this(x, index);
+    });
+    __syncthreads();
+    ranked = sh.ranked;                             // k - left
+  }
+  for (uint32_t i = tid; i < ranked; i += kThreads) {
+    const float x = sh.value[i];
+    const uint32_t index = sh.index[i];
+    uint32_t rank = 0u;
+    for (uint32_t j = 0; j < ranked; ++j) {
+      const float y = sh.value[j];
+      rank += y > x || (y == x && sh.index[j] < index);
+    }
+    if (rank < k) {
+      top[rank] = log_p(x);
+      ids[rank] = (int32_t)index;
+    }
+  }
+  // the first logits of key `equal`, by index
+  uint32_t filled = ranked;
+  const uint32_t vectors = (row.lead + row.n + V - 1) / V;
+  for (uint32_t v0 = 0; filled < k && v0 < vectors; v0 += kThreads) {
+    float x[V];
+    uint32_t fits = v0 + tid < vectors ? row.load(v0 + tid, x) : 0u;
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if ((fits >> e & 1u) && order_key(x[e]) != equal) fits &= ~(1u << e);
+    const uint32_t own = (uint32_t)__builtin_popcount(fits);
+    uint32_t upto = own;
+    for (int i = 1; i < 64; i <<= 1) {
+      const uint32_t o = __shfl_up(upto, i);
+      if ((int)(tid & 63u) >= i) upto += o;
+    }
+    __syncthreads();
+    if ((tid & 63u) == 63u) sh.wave[tid >> 6] = upto;
+    __syncthreads();
+    uint32_t place = filled + upto - own;
+    for (uint32_t w = 0; w < kThreads / 64; ++w) {
+      if (w < (tid >> 6)) place += sh.wave[w];
+      filled += sh.wave[w];
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (fits >> e & 1u) {
+        if (place < k) {
+          top[place] = log_p(x[e]);
+          ids[place] = (int32_t)((v0 + tid) * V + e - row.lead);
+        }
+        ++place;
+      }
+  }
+}
+
+// A row's outputs from its sums.
+template <bool kF32>
+__device__ void finish(const LogprobArgs& a, int64_t t, const Row<kF32>& row, const Stats& all,
+                       bool given, float mine, const float* maxima, uint32_t segments, Select& sh) {
+  const bool none = all.m == -kInf && all.s == 0.0f;   // nothing but -inf
+  const bool good = none || all.s == all.s;            // no NaN, no +inf
+  const float from = anchor(all.m), log_s = __builtin_amdgcn_logf(all.s);
+  const float nan = __builtin_nanf("");
+  auto log_p = [&](float x) {
+    return !good ? nan : x == -kInf ? -kInf : __builtin_fmaf(x - from, a.scale, -log_s * kLn2);
+  };
+  if (threadIdx.x == 0) {
+    a.logprobs[t] = given ? log_p(mine) : 0.0f;
+    a.ranks[t] = given && good ? (int32_t)all.above : -1;
+    a.entropy[t] = !good ? nan : none ? 0.0f : (log_s - all.d / all.s) * kLn2;
+    a.lse[t] = !good ? nan : none ? -kInf : __builtin_fmaf(log_s, kLn2, all.m * a.scale);
+  }
+  if (a.k == 0) return;
+  float* top = a.top + t * a.k;
+  int32_t* ids = a.ids + t * a.k;
+  if (good) {
+    select_top(row, maxima, segments, (uint32_t)a.k, top, ids, sh, log_p);
+  } else if (threadIdx.x < (uint32_t)a.k) {
+    top[threadIdx.x] = nan;
+    ids[threadIdx.x] = -1;
+  }
+}
+
+template <bool kF32>
+__device__ __forceinline__ bool token_logit(const LogprobArgs& a, int64_t t, const Row<kF32>& row,
+                                            float& mine) {
+  const int64_t token = a.tokens[t];
+  const bool given = token >= 0 && token < a.V;
+  mine = given ? row.at((uint32_t)token) : kInf;
+  return given;
+}
+
+__device__ __forceinline__ uint32_t segments_of(uint32_t lead, int64_t vocab, int per) {
+  return (lead + (uint32_t)vocab + per - 1u) / per;
+}
+
+// One workgroup per row: the pass and the selection.
+template <bool kF32>
+__global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
+  extern __shared__ float maxima[];
+  __shared__ Select sh;
+  const int64_t t = blockIdx.x;
+  const Row<kF32> row(a.logits, a.ld, t, a.V);
+  const float c = a.scale * kLog2e;
+  float mine;
+  const bool given = token_logit(a, t, row, mine);
+  const uint32_t segments = segments_of(row.lead, a.V, 8 * Row<kF32>::V);
+  const Stats all = stream(row, 0u, segments, c, mine, maxima);
+  finish(a, t, row, all, given, mine, maxima, segments, sh);
+}
+
+// Few rows: the pass over `parts` parts of each, every one of `share` segments, ...
+template <bool kF32>
+__global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobArgs a, uint32_t parts,
+                                                                uint32_t share) {
+  const int64_t t = blockIdx.x / parts;
+  const uint32_t p = blockIdx.x - (uint32_t)t * parts;
+  const Row<kF32> row(a.logits, a.ld, t, a.V);
+  const float c = a.scale * kLog2e;
+  float mine;
+  token_logit(a, t, row, mine);
+  const uint32_t segments = segments_of(row.lead, a.V, 8 * Row<kF32>::V);
+  const uint32_t first = p * share < segments ? p * share : segments;
+  const uint32_t last = first + share < segments ? first + share : segments;
+  Stats* stats = reinterpret_cast<Stats*>(a.ws);
+  float* maxima = reinterpret_cast<float*>(stats + (uint64_t)a.T * parts) +
+                  (uint64_t)blockIdx.x * share;
+  const Stats all = stream(row, first, last, c, mine, maxima);
+  if (threadIdx.x == 0) stats[blockIdx.x] = all;
+}
+
+// ... and what follows from them.
+template <bool kF32>
+__global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, uint32_t parts,
+                                                                uint32_t share) {
+  __shared__ Select sh;
+  const int64_t t = blockIdx.x;
+  const Row<kF32> row(a.logits, a.ld, t, a.V);
+  const float c = a.scale * kLog2e;
+  float mine;
+  const bool given = token_logit(a, t, row, mine);
+  const Stats* stats = reinterpret_cast<const Stats*>(a.ws) + (uint64_t)t * parts;
+  Stats all = {-kInf, 0.0f, 0.0f, 0u};
+  for (uint32_t p = threadIdx.x & 63u; p < parts; p += 64u) {
+    join(all, stats[p].m, stats[p].s, stats[p].d, c);
+    all.above += stats[p].above;
+  }
+  for (int i = 1; i < 64; i <<= 1) {
+    join(all, __shfl_xor(all.m, i), __shfl_xor(all.s, i), __shfl_xor(all.d, i), c);
+    all.above += __shfl_xor(all.above, i);
+  }
+  const float* maxima = reinterpret_cast<const float*>(reinterpret_cast<const Stats*>(a.ws) +
+                                                       (uint64_t)a.T * parts) +
+                        (uint64_t)t * parts * share;
+  finish(a, t, row, all, given, mine, maxima,
+         segments_of(row.lead, a.V, 8 * Row<kF32>::V), sh);
+}
+
+struct Plan {
+  uint32_t parts, share;        // parts of a row, segments of a part
+};
+
+// One workgroup per row where there are rows enough to fill the card (or little to
+// share), and its segment maxima fit LDS.
+Plan plan_of(bool f32, int64_t T, int64_t V) {
+  // the row may start anywhere in its first segment
+  const int64_t per = f32 ? 32 : 64, segments = (V + 2 * per - 2) / per;
+  const int64_t sweeps = (segments + kSweep - 1) / kSweep;
+  int64_t parts = (1024 + T - 1) / T;
+  const int64_t least = (segments + kMaxSegments - 1) / kMaxSegments;
+  if (parts > (sweeps + 1) / 2) parts = (sweeps + 1) / 2;
+  if (parts < least) parts = least;
+  const int64_t share = (sweeps + parts - 1) / parts * kSweep;
+  return {(uint32_t)((segments + share - 1) / share), (uint32_t)share};
+}
+
+}  // namespace
+
+size_t logprobs_workspace(bool f32, int64_t T, int64_t V, int64_t k) {
+  (void)k;
+  const Plan p = plan_of(f32, T, V);
+  if (p.parts == 1) return 0;
+  const uint64_t items = (uint64_t)T * p.parts;
+  return items * sizeof(Stats) + items * p.share * sizeof(float);
+}
+
+uint64_t logprobs_items(bool f32, int64_t T, int64_t V, int64_t k) {
+  (void)k;
+  return (uint64_t)T * plan_of(f32, T, V).parts * kThreads;
+}
+
+template <bool kF32>
+static hipError_t launch(const LogprobArgs& a, hipStream_t st) {
+  const Plan p = plan_of(kF32, a.T, a.V);
+  if (p.parts == 1) {
+    hipLaunchKernelGGL(logprob_kernel<kF32>, dim3((uint32_t)a.T), dim3(kThreads),
+                       p.share * sizeof(float), st, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(logprob_part_kernel<kF32>, dim3((uint32_t)(a.T * p.parts)), dim3(kThreads), 0,
+                     st, a, p.parts, p.share);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(logprob_join_kernel<kF32>, dim3((uint32_t)a.T), dim3(kThreads), 0, st, a,
+                     p.parts, p.share);
+  return hipGetLastError();
+}
+
+hipError_t launch_logprobs(const LogprobArgs& a, bool f32, hipStream_t st) {
+  return f32 ? launch<true>(a, st) : launch<false>(a, st);
+}
+
+}  // namespace fp8k

@@ -23,54 +23,13 @@ namespace fp8k {
 
 namespace {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// two fp32 to bf16, round to nearest even, in one instruction
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
-
-// 1 / sqrt(x), x >= 0, within 1 ulp; the instruction does not take subnormals
-__device__ __forceinline__ float rsqrt_of(float x) {
-  const bool tiny = x < 0x1p-100f;
-  const float r = __builtin_amdgcn_rsqf(tiny ? x * 0x1p+100f : x);
-  return tiny ? r * 0x1p+50f : r;
-}
-
-// E4M3 codes of 8 fp32 values divided by a static scale.  The quotient takes
-// the steps of quant8_static; for an fp32 dividend it may be off by one ulp of
-// fp32 (a bf16 one is exact), 2^-19 of an E4M3 step.
-__device__ __forceinline__ uint2 quant8_f32(const float z[8], const StaticDivisor& d) {
-  bool direct = !d.fast;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) direct |= z[e] != z[e];
-  uint32_t o[2] = {0u, 0u};
-  if (direct) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      o[e / 4] |= (uint32_t)e4m3_encode_one(z[e] / d.s) << (8 * (e & 3));
-    return make_uint2(o[0], o[1]);
-  }
-  float q[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    // s' is below 2, so what is cut here has a quotient beyond 448
-    const float x = __builtin_ldexpf(z[e], d.k);
-    const float xa = __builtin_amdgcn_fmed3f(x, -1024.0f, 1024.0f);
-    const float q0 = xa * d.r;
-    const float r = __builtin_fmaf(-q0, d.sp, xa);
-    q[e] = __builtin_amdgcn_fmed3f(__builtin_fmaf(r, d.r, q0), -kE4M3Max, kE4M3Max);
-  }
-  o[0] = e4m3_pack4_mag(q[0], q[1], q[2], q[3]) ^ d.sign;
-  o[1] = e4m3_pack4_mag(q[4], q[5], q[6], q[7]) ^ d.sign;
-  return make_uint2(o[0], o[1]);
-}
-
 // L lanes per head.  `chunks` lane groups share a token's Hq + 2 Hk heads: group
 // j takes heads j, j + chunks, ..., so that a wave's groups read neighbouring
 // heads and are mostly all at queries, at keys or at values.
-template <int L, bool kInterleaved>
+// kAxes: positions on several axes.  A lane's 8 pairs (4 where neighbours are
+// paired) may belong to different axes, so it reads their angles one by one,
+// unless the token stands at one position on all axes, as text does.
+template <int L, bool kInterleaved, bool kAxes>
 __global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, uint32_t chunks) {
   const uint32_t item = blockIdx.x * (256u / L) + threadIdx.x / L;
   const int c = threadIdx.x % L;                    // this lane's 8 values of the head
@@ -91,6 +50,16 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, uint32_t
   uint4 next = fetch(h0);                           // on its way while the angles are found
   const int64_t pos = a.positions[t], slot = a.slots[t];
   if (pos < 0 || pos >= a.max_pos) return;
+  int64_t at[4] = {pos, pos, pos, pos};
+  if (kAxes) {
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      if (i < a.axes) at[i] = a.positions[i * a.ld_pos + t];
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      if (at[i] < 0 || at[i] >= a.max_pos) return;
+  }
+  const bool apart = kAxes && (at[1] != pos || at[2] != pos || at[3] != pos);
   const bool keep = slot >= 0 && slot < a.capacity;
   const bool turns = c * 8 < a.rot;
   const int half = a.rot / 2;
@@ -102,7 +71,34 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, uint32_t
     cs[e] = 1.0f;
     sn[e] = 0.0f;
   }
-  if (turns) {
+  if (turns && apart) {
+    const bool low = kInterleaved || c * 8 < half;
+    const int j0 = kInterleaved ? c * 4 : low ? c * 8 : c * 8 - half;
+    const uint32_t inv = 65536u / (uint32_t)a.axes + 1u;      // i * inv >> 16 = i / axes, i < 2^8
+#pragma unroll
+    for (int e = 0; e < (kInterleaved ? 4 : 8); ++e) {
+      const int j = j0 + e;
+      int ax;
+      if (a.in_turn) {
+        ax = j - (int)((uint32_t)j * inv >> 16) * a.axes;
+        const int most = ax == 0 ? a.bound[0] : ax == 1 ? a.bound[1]
+                       : ax == 2 ? a.bound[2] : a.bound[3];
+        ax = j < most ? ax : 0;
+      } else {
+        ax = (j >= a.bound[0]) + (j >= a.bound[1]) + (j >= a.bound[2]);
+      }
+      const int64_t p = ax == 0 ? at[0] : ax == 1 ? at[1] : ax == 2 ? at[2] : at[3];
+      const float vc = a.cos_sin[p * a.rot + j], vs = a.cos_sin[p * a.rot + half + j];
+      if (kInterleaved) {
+        cs[2 * e] = cs[2 * e + 1] = vc;
+        sn[2 * e] = -vs;
+        sn[2 * e + 1] = vs;
+      } else {
+        cs[e] = vc;
+        sn[e] = low ? -vs : vs;
+      }
+    }
+  } else if (turns) {
     const float* row = a.cos_sin + pos * a.rot;
     if (kInterleaved) {
       const float4 vc = *reinterpret_cast<const float4*>(row + c * 4);
@@ -206,10 +202,14 @@ void launch_l(const NormRopeArgs& a, bool inter, hipStream_t st) {
   const int chunks = (heads + per - 1) / per;
   const int64_t items = a.T * chunks * L;
   const dim3 grid((uint32_t)((items + 255) / 256));
-  if (inter)
-    hipLaunchKernelGGL((norm_rope_kernel<L, true>), grid, dim3(256), 0, st, a, chunks);
+  if (a.axes > 0 && inter)
+    hipLaunchKernelGGL((norm_rope_kernel<L, true, true>), grid, dim3(256), 0, st, a, chunks);
+  else if (a.axes > 0)
+    hipLaunchKernelGGL((norm_rope_kernel<L, false, true>), grid, dim3(256), 0, st, a, chunks);
+  else if (inter)
+    hipLaunchKernelGGL((norm_rope_kernel<L, true, false>), grid, dim3(256), 0, st, a, chunks);
   else
-    hipLaunchKernelGGL((norm_rope_kernel<L, false>), grid, dim3(256), 0, st, a, chunks);
+    hipLaunchKernelGGL((norm_rope_kernel<L, false, false>), grid, dim3(256), 0, st, a, chunks);
 }
 
 }  // namespace

@@ -83,6 +83,19 @@ PyObject* matrix(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   return Py_BuildValue("NLL", pointer(*t), (long long)t->size(0), (long long)t->size(1));
 }
 
+// rows(t, dtype, device) -> (pointer, rows, columns, row stride): 2-D, unit column stride
+PyObject* rows(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  if (nargs != 3 || !THPDtype_Check(args[1])) {
+    PyErr_SetString(PyExc_TypeError, "rows(tensor, dtype, device)");
+    return nullptr;
+  }
+  const at::Tensor* t =
+      tensor_of(args[0], reinterpret_cast<THPDtype*>(args[1])->scalar_type, args[2]);
+  if (!t || t->dim() != 2 || (t->size(1) > 1 && t->stride(1) != 1)) Py_RETURN_NONE;
+  const long long n = t->size(0), width = t->size(1);
+  return Py_BuildValue("NLLL", pointer(*t), n, width, n > 1 ? (long long)t->stride(0) : width);
+}
+
 // caches(key, value, device) -> (key pointer, value pointer, blocks, block size, H, D):
 // contiguous uint8 [blocks, block size, H, D], of one shape
 PyObject* caches(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
@@ -115,6 +128,7 @@ PyMethodDef methods[] = {
     {"heads", (PyCFunction)(void (*)(void))guarded<heads>, METH_FASTCALL, nullptr},
     {"table", (PyCFunction)(void (*)(void))guarded<table>, METH_FASTCALL, nullptr},
     {"matrix", (PyCFunction)(void (*)(void))guarded<matrix>, METH_FASTCALL, nullptr},
+    {"rows", (PyCFunction)(void (*)(void))guarded<rows>, METH_FASTCALL, nullptr},
     {"caches", (PyCFunction)(void (*)(void))guarded<caches>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
