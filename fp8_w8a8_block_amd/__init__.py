@@ -16,5 +16,5 @@ from ._lib import (  # noqa: F401
 )
 from ._step import (  # noqa: F401
     MAX_TOP, add_rms_norm, add_rms_norm_quant, int4_linear, int4_pack, int4_quant_weight,
-    logprobs_workspace_bytes, qk_norm_mrope_cache, token_logprobs,
+    int4_workspace_bytes, logprobs_workspace_bytes, qk_norm_mrope_cache, token_logprobs,
 )

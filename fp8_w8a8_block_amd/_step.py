@@ -25,7 +25,7 @@ _MROPE = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _i64, _i64, _int
           _int, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp]
 _PACK = [_vp, _i64, _vp, _i64, _i64]
 _QUANT = [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64]
-_INT4 = [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64]
+_INT4 = [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _sz]
 _PROBS = [_vp, _int, _i64, _vp, _f32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz]
 
 _SIGS = {
@@ -37,6 +37,7 @@ _SIGS = {
     "fp8_validate_int4_pack": (_int, _PACK),
     "fp8_int4_quant_weight": (_int, _QUANT + [_vp]),
     "fp8_validate_int4_quant_weight": (_int, _QUANT),
+    "fp8_int4_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "fp8_int4_linear": (_int, _INT4 + [_vp]),
     "fp8_validate_int4_linear": (_int, _INT4),
     "fp8_logprobs_workspace_bytes": (_sz, [_int, _i64, _i64, _i64]),
@@ -204,10 +205,16 @@ def int4_quant_weight(w, group=128, symmetric=False):
     return codes, scales, zeros
 
 
-def int4_linear(x, codes, scales, zeros=None, out=None):
+def int4_workspace_bytes(M, N, K):
+    """Workspace bytes with which int4_linear cuts K into runs (0: it does not)."""
+    return int(lib().fp8_int4_workspace_bytes(int(M), int(N), int(K)))
+
+
+def int4_linear(x, codes, scales, zeros=None, out=None, workspace=None):
     """out = x . W^T of bf16 x [M, K] with 4-bit weights: packed codes uint8 [N, K / 2],
     scales float32 [N, K / group], zero points uint8 of the same shape (None: 8)
-    -> bf16 [M, N]."""
+    -> bf16 [M, N].  Sizes that cut K into runs (int4_workspace_bytes > 0) get a
+    workspace, allocated here unless given."""
     dev = _device_of(x, "x")
     xp, M, K, ld_x = _rows(x, "x", torch.bfloat16, dev)
     cp, N, half = _matrix(codes, "codes", torch.uint8, dev)
@@ -222,8 +229,18 @@ def int4_linear(x, codes, scales, zeros=None, out=None):
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     op, _, _, ld_out = _rows(out, "out", torch.bfloat16, dev, (M, N))
-    _check(_call(dev, lambda: lib().fp8_int4_linear(xp, ld_x, cp, sp, zp, K // groups, op, ld_out, M, N,
-                                                    K, _raw_stream(dev))))
+
+    def call():
+        l, ws = lib(), workspace
+        if ws is None and M > 4:
+            n = l.fp8_int4_workspace_bytes(M, N, K)
+            if n:
+                ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        ws_ptr, ws_len = _workspace(ws, dev)
+        return l.fp8_int4_linear(xp, ld_x, cp, sp, zp, K // groups, op, ld_out, M, N, K, ws_ptr, ws_len,
+                                 _raw_stream(dev))
+
+    _check(_call(dev, call))
     return out
 
 

@@ -7,6 +7,8 @@
 // one and-or turn two codes of the packed layout into a pair of the matrix
 // unit's operand.  The group's sum of x is one more column of the product, by a
 // column of ones, and comes out in the lanes and registers that need it.
+#include <type_traits>
+
 #include "device_common.h"
 #include "launch.h"
 #include "step_launch.h"
@@ -17,6 +19,7 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // ---- packing and quantization ----------------------------------------------
 
@@ -98,10 +101,10 @@ __device__ __forceinline__ bf16x8 operand(uint32_t d) {
 // q = lane / 16.  A product takes 8 values from each quarter and must stay within
 // one group, so where groups are shorter than a block the quarters' dwords trade
 // places: across the wave's halves for 64, and across its rows of 16, too, for 32.
-// Afterwards dword j holds the values from x_offset<G>(j, q) on.
-template <int G>
+// Afterwards dword j holds the values from x_offset<S>(j, q) on.
+template <int S>
 __device__ __forceinline__ void spread(uint32_t (&d)[4]) {
-  if (G <= 64) {
+  if (S <= 64) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const auto r = __builtin_amdgcn_permlane32_swap(d[j], d[j + 2], false, false);
@@ -109,7 +112,7 @@ __device__ __forceinline__ void spread(uint32_t (&d)[4]) {
       d[j + 2] = r[1];
     }
   }
-  if (G == 32) {
+  if (S == 32) {
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
       const auto r = __builtin_amdgcn_permlane16_swap(d[j], d[j + 1], false, false);
@@ -119,164 +122,533 @@ __device__ __forceinline__ void spread(uint32_t (&d)[4]) {
   }
 }
 
-template <int G>
+template <int S>
 __device__ __forceinline__ int x_offset(int j, int q) {
-  if (G == 128) return q * 32 + j * 8;
-  if (G == 64) return (j >> 1) * 64 + (q & 1) * 32 + (q >> 1) * 16 + (j & 1) * 8;
+  if (S == 128) return q * 32 + j * 8;
+  if (S == 64) return (j >> 1) * 64 + (q & 1) * 32 + (q >> 1) * 16 + (j & 1) * 8;
   return j * 32 + q * 8;
 }
 
-// Up to 16 MT rows of x with 16 NT rows of the weight per workgroup, whose W waves
-// share K: wave w takes every W-th block of 128 values.
-template <int MT, int NT, int W, int G, bool kZeros>
-__global__ __launch_bounds__(64 * W) void int4_rows_kernel(Int4Args a, uint32_t m_tiles) {
-  __shared__ float part[W][MT * 16][NT * 16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
-  const uint32_t tile = blockIdx.x / m_tiles;
-  const int64_t n0 = (int64_t)tile * (16 * NT);
-  const int64_t m0 = (int64_t)(blockIdx.x - tile * m_tiles) * (16 * MT);
-  const int blocks = a.K / 128;
-  constexpr int GPB = 128 / G;                      // groups of a block
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
 
+__device__ __forceinline__ void store_bf16(const Int4Args& a, int64_t m, int64_t n, float v) {
+  if (m < a.M && n < a.N) a.out[m * a.ld_out + n] = (uint16_t)pack_bf16(v, v);
+}
+
+constexpr int kFewGroups = 32;                // groups of a row that LDS holds, for each wave
+
+// Up to 4 rows of x with 16 rows of the weight.  The 16 rows of the matrix unit's
+// operand are the 4 rows of x times the 4 products j of a block: row 4 m + j holds
+// the values of x's row m that product j multiplies, so one load a block brings
+// all of x, and product j's result is right where row = 4 m + j: in register j of
+// quarter m.  Column n, quarter m of the wave is output (m, n).  The groups' sums of
+// x are the same product with ones.
+//
+// The workgroup's waves share K: each takes a run of units of four blocks, the next
+// of which is in flight while it works on one.
+template <int G, bool kZeros>
+__global__ __launch_bounds__(1024) void int4_few_kernel(Int4Args a) {
+  constexpr int GPB = 128 / G, J = 4 / GPB;         // products of a group
+  constexpr int kStage = kFewGroups / 4;            // of which a thread brings every 4 waves-th
+  extern __shared__ float2 few_lds[];               // scales and offsets; then the waves' parts
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = (int)blockDim.x >> 6;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int blocks = a.K / 128, units = (blocks + 3) / 4;
+  const int most = kFewGroups * waves / (4 * GPB);  // units of a chunk of K
   // rows behind the last are read as the last and not stored
-  const uint8_t* wp[NT];
-  const float* sp[NT];
-  const uint8_t* zp[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    int64_t n = n0 + 16 * t + l16;
-    n = n < a.N ? n : a.N - 1;
-    wp[t] = a.codes + n * (a.K / 2) + q * 16;
-    sp[t] = a.scales + n * (a.K / G);
-    zp[t] = kZeros ? a.zeros + n * (a.K / G) : nullptr;
-  }
-  const uint16_t* xp[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    int64_t m = m0 + 16 * i + l16;
-    m = m < a.M ? m : a.M - 1;
-    xp[i] = a.x + m * a.ld_x;
-  }
+  const int rows = (int)(a.N - n0 < 16 ? a.N - n0 : 16);
+  const int64_t m = (l16 >> 2) < a.M ? l16 >> 2 : a.M - 1;
+  const uint8_t* w = a.codes + n0 * (a.K / 2);
+  const uint32_t wo = (uint32_t)(l16 < rows ? l16 : rows - 1) * (uint32_t)(a.K / 2) + q * 16;
+  const uint16_t* x = a.x + m * a.ld_x + x_offset<G>(l16 & 3, q);
 
+  struct Unit {
+    u32x4 w[4];
+    bf16x8 x[4];
+  };
+  auto fetch = [&](Unit& u, int at) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = at * 4 + i < blocks ? at * 4 + i : blocks - 1;
+      u.w[i] = *reinterpret_cast<const u32x4*>(w + (uint32_t)b * 64u + wo);
+      u.x[i] = *reinterpret_cast<const bf16x8*>(x + b * 128);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
   const bf16x8 ones = __builtin_bit_cast(
       bf16x8, make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u));
+  float acc = 0.0f;
+  for (int c0 = 0; c0 < units; c0 += most) {
+    const int cn = units - c0 < most ? units - c0 : most;
+    const int held = (cn * 4 < blocks - c0 * 4 ? cn * 4 : blocks - c0 * 4) * GPB;
+    const int pitch = held | 1;
+    if (c0) __syncthreads();
+    // the groups of 16 rows, neighbouring threads along a row: read where they are
+    // used, 16 rows at 4 bytes, they cost more requests than the codes
+    float gs[kStage];
+    uint32_t gz[kStage];
+    const int gr = (int)__umulhi(threadIdx.x, 0xffffffffu / (uint32_t)(4 * waves) + 1u);
+    const int gc = (int)threadIdx.x - gr * 4 * waves;                // threadIdx.x / (4 waves), the rest
+    const float* gs0 = a.scales + n0 * (a.K / G) + c0 * 4 * GPB;
+    const uint8_t* gz0 = kZeros ? a.zeros + n0 * (a.K / G) + c0 * 4 * GPB : nullptr;
+    const uint32_t go = (uint32_t)(gr < rows ? gr : rows - 1) * (uint32_t)(a.K / G);
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) {
+      if (i * 4 * waves >= held) break;             // all of the workgroup
+      const int g = gc + i * 4 * waves < held ? gc + i * 4 * waves : held - 1;
+      gs[i] = gs0[go + (uint32_t)g];
+      if (kZeros) gz[i] = gz0[go + (uint32_t)g];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const int first = c0 + (int)((uint32_t)cn * wave / waves);
+    const int last = c0 + (int)((uint32_t)cn * (wave + 1) / waves);
+    Unit here, next;
+    fetch(here, first < last ? first : c0);
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) {
+      const int g = gc + i * 4 * waves;
+      if (i * 4 * waves >= held) break;
+      if (g < held)
+        few_lds[gr * pitch + g] = make_float2(gs[i], 16.0f + (kZeros ? (float)gz[i] : 8.0f));
+    }
+    __syncthreads();
+    const float2* of = few_lds + l16 * pitch;
+    auto multiply = [&](const Unit& u, int at) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (at * 4 + i >= blocks) break;            // all of the wave
+        uint32_t d[4] = {u.w[i].x, u.w[i].y, u.w[i].z, u.w[i].w};
+        spread<G>(d);
+        const f32x4 zero = {}, sum = mfma(u.x[i], ones, zero);
+        float p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = mfma(u.x[i], operand(d[j]), zero)[j];
+#pragma unroll
+        for (int g = 0; g < GPB; ++g) {
+          float v = p[g * J], o = sum[g * J];
+#pragma unroll
+          for (int j = 1; j < J; ++j) {
+            v += p[g * J + j];
+            o += sum[g * J + j];
+          }
+          const float2 sz = of[((at - c0) * 4 + i) * GPB + g];
+          acc = __builtin_fmaf(sz.x, __builtin_fmaf(-sz.y, o, v), acc);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    for (int at = first; at < last; at += 2) {
+      fetch(next, at + 1 < last ? at + 1 : at);
+      multiply(here, at);
+      if (at + 1 >= last) break;
+      fetch(here, at + 2 < last ? at + 2 : at);
+      multiply(next, at + 1);
+    }
+  }
+
+  if (waves > 1) {
+    float* part = reinterpret_cast<float*>(few_lds);
+    __syncthreads();
+    part[wave * 64 + lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll 4
+    for (int i = 1; i < waves; ++i) acc += part[i * 64 + lane];
+  }
+  store_bf16(a, q, n0 + l16, acc);
+}
+
+// Sum of 8 bf16 values and what v holds.
+__device__ __forceinline__ float sum8(u32x4 x) {
+  float v = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t pair = x[e];
+    v = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair),
+                                        __builtin_bit_cast(bf16x2, 0x3f803f80u), v, false);
+  }
+  return v;
+}
+
+// Sum over the L neighbouring lanes (4, 8 or 16) of each L, in all of them.
+template <int L>
+__device__ __forceinline__ float sum_lanes(float v) {
+  auto other = [](float x, auto ctrl) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+        0, (int)__float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  v += other(v, std::integral_constant<int, 0xb1>());               // lane ^ 1
+  v += other(v, std::integral_constant<int, 0x4e>());               // lane ^ 2
+  if (L >= 8) v += other(v, std::integral_constant<int, 0x141>());  // 7 - lane of 8
+  if (L >= 16) v += other(v, std::integral_constant<int, 0x140>()); // 15 - lane of 16
+  return v;
+}
+
+// 16 MT rows of x with 16 NT WN rows of the weight per workgroup of WN x WK waves, over
+// a run of K (`runs` of them; more than one: the sums go to a.parts and are added
+// by int4_join_kernel).  The waves of WK take every WK-th block of K.  x goes through
+// LDS, KB blocks at a time, with its sums by groups, and so do the scales and
+// offsets, kTileGroups at a time; both twice, the next while the last are in use.
+// The codes come straight to the waves that multiply them, kAhead blocks ahead.
+template <int MT, int NT, int WN, int WK, int G, bool kZeros>
+__global__ __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_eu(MT >= 4 ? 3 : 4)))
+void int4_tile_kernel(Int4Args a, uint32_t m_tiles, uint32_t runs) {
+  constexpr int GPB = 128 / G, J = 4 / GPB, kThreads = 64 * WN * WK;
+  constexpr int kRowsM = 16 * MT, kRowsN = 16 * NT * WN;
+  constexpr int kAhead = MT >= 4 ? 2 : 4;
+  constexpr int KB = MT >= 4 ? 1 : WK > 4 ? 8 : 4;                  // blocks of x in LDS
+  constexpr int kTurns = KB / WK;                                   // of a wave with them
+  constexpr int kPitch = KB * 128 + 8;                              // of a row of x there
+  constexpr int kStage = kRowsM * KB * 16 / kThreads;               // 16-byte pieces a thread
+  constexpr int kTileGroups = MT >= 4 && GPB < 4 ? 8 : 16 * WK;
+  constexpr int kHeld = kTileGroups / GPB;                          // blocks whose groups LDS holds
+  constexpr int kStageG = kRowsN * kTileGroups / kThreads;
+  static_assert(kRowsM * KB * 16 % kThreads == 0 && kRowsN * kTileGroups % kThreads == 0 &&
+                kHeld % (4 * WK) == 0 && 4 % kTurns == 0, "");
+  typedef std::conditional_t<kZeros, float2, float> Group;          // scale (and offset)
+  __shared__ uint16_t xs[2][kRowsM * kPitch];
+  __shared__ float sums[2][KB * GPB][kRowsM];
+  __shared__ Group gs[2][kRowsN * (kTileGroups + 1)];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave / WK, wk = wave % WK;
+  // neighbouring workgroups take the m tiles of one n tile, then the next run
+  const uint32_t run = blockIdx.x % runs, rest = blockIdx.x / runs;
+  const int64_t n0 = (int64_t)(rest / m_tiles) * kRowsN;
+  const int64_t m0 = (int64_t)(rest % m_tiles) * kRowsM;
+  const int blocks = a.K / 128;
+  const int first = (int)((uint64_t)(uint32_t)blocks * run / runs);
+  const int last = (int)((uint64_t)(uint32_t)blocks * (run + 1) / runs);
+
+  // rows of the weight behind the last are read as the last and not stored
+  const int rows_n = (int)(a.N - n0 < kRowsN ? a.N - n0 : kRowsN);
+  const int rows_m = (int)(a.M - m0 < kRowsM ? a.M - m0 : kRowsM);
+  const uint8_t* wb = a.codes + n0 * (a.K / 2);
+  uint32_t wo[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int n = 16 * (wn * NT + t) + l16;
+    wo[t] = (uint32_t)(n < rows_n ? n : rows_n - 1) * (uint32_t)(a.K / 2) + q * 16;
+  }
+  auto fetch_w = [&](u32x4 (&r)[NT], int b) __attribute__((always_inline)) {
+    b = b < blocks ? b : blocks - 1;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      r[t] = *reinterpret_cast<const u32x4*>(wb + (uint32_t)b * 64u + wo[t]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // rows of x behind the last: few rows skip them (what LDS holds in their place goes
+  // into results that are not stored), many read the last again, without a branch
+  constexpr bool kSkip = MT == 1;
+  u32x4 stage[kStage];
+  auto fetch_x = [&](int b0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) {
+      const int e = i * kThreads + threadIdx.x, r = e / (KB * 16), c = e % (KB * 16);
+      const int b = b0 + c / 16 < blocks ? b0 + c / 16 : blocks - 1;
+      if (kSkip && r >= rows_m) continue;
+      const int64_t m = m0 + (r < rows_m ? r : rows_m - 1);
+      stage[i] = *reinterpret_cast<const u32x4*>(a.x + m * a.ld_x + b * 128 + c % 16 * 8);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto keep_x = [&](int buffer) __attribute__((always_inline)) {
+    constexpr int L = G / 8;                        // pieces of a group
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) {
+      const int e = i * kThreads + threadIdx.x, r = e / (KB * 16), c = e % (KB * 16);
+      if (kSkip && r >= rows_m) continue;
+      *reinterpret_cast<u32x4*>(&xs[buffer][r * kPitch + c * 8]) = stage[i];
+      const float v = sum_lanes<L>(sum8(stage[i]));
+      if (c % L == 0) sums[buffer][c / L][r] = v;
+    }
+  };
+  float stage_s[kStageG];
+  uint8_t stage_z[kStageG];
+  const int per_row = a.K / G;
+  const float* gs0 = a.scales + n0 * per_row;
+  const uint8_t* gz0 = kZeros ? a.zeros + n0 * per_row : nullptr;
+  auto fetch_g = [&](int b0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kStageG; ++i) {
+      const int e = i * kThreads + threadIdx.x, r = e / kTileGroups, c = e % kTileGroups;
+      const int g = b0 * GPB + c < per_row ? b0 * GPB + c : per_row - 1;
+      const uint32_t at = (uint32_t)(r < rows_n ? r : rows_n - 1) * (uint32_t)per_row + (uint32_t)g;
+      stage_s[i] = gs0[at];
+      if (kZeros) stage_z[i] = gz0[at];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto keep_g = [&](int buffer) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kStageG; ++i) {
+      const int e = i * kThreads + threadIdx.x, r = e / kTileGroups, c = e % kTileGroups;
+      Group& to = gs[buffer][r * (kTileGroups + 1) + c];
+      if constexpr (kZeros)
+        to = make_float2(stage_s[i], 16.0f + (float)stage_z[i]);
+      else
+        to = stage_s[i];
+    }
+  };
+  auto read_x = [&](bf16x8 (&r)[MT], const uint16_t* xb, int k) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      r[i] = *reinterpret_cast<const bf16x8*>(xb + i * 16 * kPitch + x_offset<G>(k, q));
+  };
+
   f32x4 acc[MT][NT] = {};
-  for (int b = wave; b < blocks; b += W) {
-    uint32_t d[NT][4];
-    float s[NT][GPB], z[NT][GPB];
-    bf16x8 x[MT][4];
+  u32x4 w[kAhead][NT];
+  fetch_x(first);
+  fetch_g(first);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const uint4 v = *reinterpret_cast<const uint4*>(wp[t] + (int64_t)b * 64);
-      d[t][0] = v.x;
-      d[t][1] = v.y;
-      d[t][2] = v.z;
-      d[t][3] = v.w;
+  for (int j = 0; j < kAhead; ++j) fetch_w(w[j], first + j * WK + wk);
+  keep_x(0);
+  keep_g(0);
+  fetch_x(first + KB);
+  __syncthreads();
+  int buffer = 0, gbuffer = 0;
+  for (int b = first; b < last; b += 4 * WK) {
+    const int at = (b - first) % kHeld;             // among the blocks whose groups are held
+    if (at == 0) fetch_g(b + kHeld);
 #pragma unroll
-      for (int g = 0; g < GPB; ++g) {
-        s[t][g] = sp[t][b * GPB + g];
-        z[t][g] = 16.0f + (kZeros ? (float)zp[t][b * GPB + g] : 8.0f);
+    for (int j = 0; j < 4; ++j) {
+      const int mine = j * WK + wk;                 // this wave's block, counted from b
+      if (b + mine < last) {
+        const int held = mine % KB;                 // its place in LDS
+        const uint16_t* xb = &xs[buffer][l16 * kPitch + held * 128];
+        const Group* gb =
+            &gs[gbuffer][(wn * NT * 16 + l16) * (kTileGroups + 1) + (at + mine) * GPB];
+        uint32_t d[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          d[t][0] = w[j % kAhead][t].x;
+          d[t][1] = w[j % kAhead][t].y;
+          d[t][2] = w[j % kAhead][t].z;
+          d[t][3] = w[j % kAhead][t].w;
+          spread<G>(d[t]);
+        }
+        bf16x8 x[MT];
+#pragma unroll
+        for (int g = 0; g < GPB; ++g) {
+          // the sums start at what the offsets make of the group's sum of x
+          Group sz[NT];
+          f32x4 p[MT][NT];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) sz[t] = gb[t * 16 * (kTileGroups + 1) + g];
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            const f32x4 sum =
+                *reinterpret_cast<const f32x4*>(&sums[buffer][held * GPB + g][16 * i + 4 * q]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              if constexpr (kZeros)
+                p[i][t] = sum * -sz[t].y;
+              else
+                p[i][t] = sum * -24.0f;
+            }
+          }
+#pragma unroll
+          for (int k = g * J; k < (g + 1) * J; ++k) {
+            read_x(x, xb, k);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const bf16x8 o = operand(d[t][k]);
+#pragma unroll
+              for (int i = 0; i < MT; ++i) p[i][t] = mfma(x[i], o, p[i][t]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float s;
+            if constexpr (kZeros)
+              s = sz[t].x;
+            else
+              s = sz[t];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[i][t][e] = __builtin_fmaf(s, p[i][t][e], acc[i][t][e]);
+              asm volatile("" : "+v"(acc[i][t]));   // here, not after the next group's products
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      fetch_w(w[j % kAhead], b + mine + kAhead * WK);
+      if (j % kTurns == kTurns - 1) {               // the next blocks of x
+        buffer ^= 1;
+        keep_x(buffer);
+        if (j == 3 && at + 4 * WK == kHeld) keep_g(gbuffer ^ 1);
+        fetch_x(b + (j + 1) * WK + KB);
+        __syncthreads();
       }
     }
+    if (at + 4 * WK == kHeld) gbuffer ^= 1;
+  }
+
+  if (WK > 1) {
+    // the waves of a tile add up their parts, in order; xs is free behind the barrier
+    constexpr int kTile = MT * NT * 256;
+    static_assert(sizeof(xs) >= sizeof(float) * WN * WK * kTile, "");
+    float* part = reinterpret_cast<float*>(xs);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[i][j] = *reinterpret_cast<const bf16x8*>(xp[i] + (int64_t)b * 128 + x_offset<G>(j, q));
-#pragma unroll
-    for (int t = 0; t < NT; ++t) spread<G>(d[t]);
-#pragma unroll
-    for (int g = 0; g < GPB; ++g) {
-      constexpr int J = 4 / GPB;                    // products of a group
-      f32x4 sum[MT] = {}, p[MT][NT] = {};
-#pragma unroll
-      for (int j = g * J; j < (g + 1) * J; ++j) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-          sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i][j], ones, sum[i], 0, 0, 0);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const bf16x8 w = operand(d[t][j]);
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-            p[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i][j], w, p[i][t], 0, 0, 0);
-        }
-      }
-#pragma unroll
       for (int t = 0; t < NT; ++t)
+        *reinterpret_cast<f32x4*>(&part[((wave * MT + i) * NT + t) * 256 + lane * 4]) = acc[i][t];
+    __syncthreads();
+    if (wk != 0) return;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+    for (int o = 1; o < WK; ++o)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[i][t][r] = __builtin_fmaf(
-                s[t][g], __builtin_fmaf(-z[t][g], sum[i][r], p[i][t][r]), acc[i][t][r]);
-    }
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          acc[i][t] += *reinterpret_cast<const f32x4*>(
+              &part[(((wave + o) * MT + i) * NT + t) * 256 + lane * 4]);
   }
-
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) part[wave][16 * i + 4 * q + r][16 * t + l16] = acc[i][t][r];
-  __syncthreads();
-  for (int e = threadIdx.x; e < MT * NT * 256; e += 64 * W) {
-    const int m = e / (16 * NT), n = e % (16 * NT);
-    float v = part[0][m][n];
+      for (int e = 0; e < 4; ++e) {
+        const int64_t m = m0 + 16 * i + 4 * q + e;
+        const int64_t n = n0 + 16 * (wn * NT + t) + l16;
+        if (runs == 1)
+          store_bf16(a, m, n, acc[i][t][e]);
+        else if (m < a.M && n < a.N)
+          a.parts[((int64_t)run * a.M + m) * a.N + n] = acc[i][t][e];
+      }
+}
+
+// The runs' sums, added in the order of K: a row of out per blockIdx.y.
+__global__ __launch_bounds__(256) void int4_join_kernel(Int4Args a, uint32_t runs) {
+  const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, m = blockIdx.y;
+  const int64_t total = a.M * a.N;
+  const float* part = a.parts + m * a.N + n;
+  if (n + 4 <= a.N && a.N % 4 == 0) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(part);
+#pragma unroll 4
+    for (uint32_t r = 1; r < runs; ++r) v += *reinterpret_cast<const f32x4*>(part + r * total);
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += part[w][m][n];
-    if (m0 + m < a.M && n0 + n < a.N)
-      a.out[(m0 + m) * a.ld_out + n0 + n] = (uint16_t)pack_bf16(v, v);
+    for (int e = 0; e < 4; ++e) store_bf16(a, m, n + e, v[e]);
+    return;
+  }
+  for (int e = 0; e < 4 && n + e < a.N; ++e) {
+    float v = part[e];
+    for (uint32_t r = 1; r < runs; ++r) v += part[r * total + e];
+    store_bf16(a, m, n + e, v);
   }
 }
 
-struct RowsPlan {
-  int mt, nt;
+// The kernel's tile (m 0: int4_few_kernel), its workgroups' waves, runs of K.
+struct Plan {
+  uint32_t m, n, waves, runs;
 };
 
-RowsPlan rows_plan(int64_t M, int64_t N) {
-  const int mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  const int nt = N >= 64 * 1024 || mt == 4 ? 4 : N >= 16 * 1024 || mt == 2 ? 2 : 1;
-  return {mt, nt};
-}
-
-uint64_t rows_grid(int64_t M, int64_t N) {
-  const RowsPlan p = rows_plan(M, N);
-  return (uint64_t)((N + 16 * p.nt - 1) / (16 * p.nt)) * (uint64_t)((M + 16 * p.mt - 1) / (16 * p.mt));
-}
-
-template <int MT, int NT, int W>
-void launch_rows(const Int4Args& a, int group, hipStream_t st) {
-  const uint32_t m_tiles = (uint32_t)((a.M + 16 * MT - 1) / (16 * MT));
-  const dim3 grid((uint32_t)rows_grid(a.M, a.N)), block(64 * W);
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, a, m_tiles); };
-  switch (group * 2 + (a.zeros != nullptr)) {
-    case 64: go(int4_rows_kernel<MT, NT, W, 32, false>); break;
-    case 65: go(int4_rows_kernel<MT, NT, W, 32, true>); break;
-    case 128: go(int4_rows_kernel<MT, NT, W, 64, false>); break;
-    case 129: go(int4_rows_kernel<MT, NT, W, 64, true>); break;
-    case 256: go(int4_rows_kernel<MT, NT, W, 128, false>); break;
-    default: go(int4_rows_kernel<MT, NT, W, 128, true>); break;
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  const int64_t blocks = K / 128, units = (blocks + 3) / 4, tiles16 = (N + 15) / 16;
+  auto runs_of = [&](int64_t m, int64_t n, int64_t want) {
+    const int64_t tiles = ((M + m - 1) / m) * ((N + n - 1) / n);
+    int64_t runs = tiles < want ? want / tiles : 1, most = blocks / 8;
+    // of 8 blocks at least, of 4 while compute units are idle
+    if (tiles * most < 256) most = blocks / 4 < 256 / tiles ? blocks / 4 : 256 / tiles;
+    runs = runs < most ? runs : most;
+    return (uint32_t)(runs < 1 ? 1 : runs);
+  };
+  if (M <= 4 && tiles16 <= 2048) {
+    // waves until all workgroups are resident at once, 16 of them to a compute unit
+    int64_t waves = 16;
+    while (waves > 2 && 256 * (16 / waves) < tiles16) waves /= 2;
+    if (waves > units) waves = units;
+    const int64_t per = (units + waves - 1) / waves;
+    return {0, 16, (uint32_t)((units + per - 1) / per), 1};
   }
+  if (M <= 16) {
+    if (N >= 64 * 1024) return {16, 128, 8, 1};
+    if (N >= 8 * 1024) return {16, 64, 8, 1};
+    // x read for every 32 or 16 rows of the weight: while that is little
+    const uint32_t n = N >= 6 * 1024 ? 32 : 16;
+    if (M * K * 2 * ((N + n - 1) / n) <= 40 << 20) return {16, n, 8, 1};
+    return {16, 128, 8, runs_of(16, 128, 256)};
+  }
+  if (M <= 32) return {32, 128, 8, runs_of(32, 128, 256)};
+  return {64, 128, 4, runs_of(64, 128, 512)};
+}
+
+uint64_t grid_of(const Plan& p, int64_t M, int64_t N) {
+  const uint64_t m = p.m ? p.m : 4;
+  return ((uint64_t)N + p.n - 1) / p.n * (((uint64_t)M + m - 1) / m) * p.runs;
+}
+
+template <typename F>
+void with_groups(const Int4Args& a, int group, F f) {
+  switch (group * 2 + (a.zeros != nullptr)) {
+    case 64: f(std::integral_constant<int, 32>(), std::false_type()); break;
+    case 65: f(std::integral_constant<int, 32>(), std::true_type()); break;
+    case 128: f(std::integral_constant<int, 64>(), std::false_type()); break;
+    case 129: f(std::integral_constant<int, 64>(), std::true_type()); break;
+    case 256: f(std::integral_constant<int, 128>(), std::false_type()); break;
+    default: f(std::integral_constant<int, 128>(), std::true_type()); break;
+  }
+}
+
+template <int MT, int NT, int WN, int WK>
+void launch_tile(const Int4Args& a, const Plan& p, int group, hipStream_t st) {
+  const dim3 grid((uint32_t)grid_of(p, a.M, a.N));
+  const uint32_t m_tiles = (uint32_t)((a.M + 16 * MT - 1) / (16 * MT));
+  with_groups(a, group, [&](auto g, auto zeros) {
+    hipLaunchKernelGGL(
+        (int4_tile_kernel<MT, NT, WN, WK, decltype(g)::value, decltype(zeros)::value>), grid,
+        dim3(64 * WN * WK), 0, st, a, m_tiles, p.runs);
+  });
+}
+
+void launch_few(const Int4Args& a, const Plan& p, int group, hipStream_t st) {
+  const uint32_t groups = (uint32_t)(a.K / group);
+  const uint32_t held = groups < kFewGroups * p.waves ? groups : kFewGroups * p.waves;
+  uint32_t lds = 16u * (held | 1u) * sizeof(float2);
+  if (lds < p.waves * 256u) lds = p.waves * 256u;
+  with_groups(a, group, [&](auto g, auto zeros) {
+    hipLaunchKernelGGL((int4_few_kernel<decltype(g)::value, decltype(zeros)::value>),
+                       dim3((uint32_t)grid_of(p, a.M, a.N)), dim3(64 * p.waves), lds, st, a);
+  });
 }
 
 }  // namespace
 
 uint64_t int4_linear_items(int64_t M, int64_t N, int64_t K) {
-  (void)K;
-  return rows_grid(M, N) * 512u;
+  const Plan p = plan_of(M, N, K);
+  return grid_of(p, M, N) * 64u * p.waves;
+}
+
+size_t int4_workspace(int64_t M, int64_t N, int64_t K) {
+  const Plan p = plan_of(M, N, K);
+  return p.runs > 1 ? (size_t)p.runs * (size_t)M * (size_t)N * sizeof(float) : 0;
 }
 
 hipError_t launch_int4_linear(const Int4Args& a, int group, hipStream_t st) {
-  const RowsPlan p = rows_plan(a.M, a.N);
-  switch (p.mt * 8 + p.nt) {
-    case 9: launch_rows<1, 1, 8>(a, group, st); break;
-    case 10: launch_rows<1, 2, 8>(a, group, st); break;
-    case 12: launch_rows<1, 4, 8>(a, group, st); break;
-    case 18: launch_rows<2, 2, 8>(a, group, st); break;
-    case 20: launch_rows<2, 4, 4>(a, group, st); break;
-    default: launch_rows<4, 4, 4>(a, group, st); break;
+  Plan p = plan_of(a.M, a.N, a.K);
+  if (!a.parts) p.runs = 1;
+  switch (p.m * 1024 + p.n) {
+    case 16: launch_few(a, p, group, st); break;
+    case 16 * 1024 + 16: launch_tile<1, 1, 1, 8>(a, p, group, st); break;
+    case 16 * 1024 + 32: launch_tile<1, 1, 2, 4>(a, p, group, st); break;
+    case 16 * 1024 + 64: launch_tile<1, 1, 4, 2>(a, p, group, st); break;
+    case 16 * 1024 + 128: launch_tile<1, 1, 8, 1>(a, p, group, st); break;
+    case 32 * 1024 + 128: launch_tile<2, 1, 8, 1>(a, p, group, st); break;
+    case 64 * 1024 + 128: launch_tile<4, 2, 4, 1>(a, p, group, st); break;
+    default: return hipErrorInvalidConfiguration;
   }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.runs == 1) return e;
+  hipLaunchKernelGGL(int4_join_kernel, dim3((uint32_t)((a.N + 1023) / 1024), (uint32_t)a.M),
+                     dim3(256), 0, st, a, p.runs);
   return hipGetLastError();
 }
 

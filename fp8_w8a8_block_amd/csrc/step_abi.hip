@@ -38,6 +38,12 @@ bool weight_shape(int64_t N, int64_t K) {
   return N >= 0 && N < kMaxDim && K > 0 && K % 128 == 0 && K < kMaxDim && N <= kMaxElems / K;
 }
 
+// sizes of a product of M rows; a tile's rows of the weight are counted in 32 bits
+bool product_shape(int64_t M, int64_t N, int64_t K) {
+  return weight_shape(N, K) && N > 0 && K < ((int64_t)1 << 24) && M >= 0 && M < kMaxDim &&
+         M <= kMaxElems / K && M <= kMaxElems / N;
+}
+
 // The axes' pairs in the form that the kernel takes; false if they do not fit.
 bool axes_of(int64_t A, const int64_t* sections, int order, int64_t half, fp8k::NormRopeArgs* a) {
   int64_t sum = 0;
@@ -264,10 +270,9 @@ fp8_status fp8_int4_quant_weight(const uint16_t* w, int64_t ld_w, uint8_t* codes
 fp8_status fp8_validate_int4_linear(const uint16_t* x, int64_t ld_x, const uint8_t* codes,
                                     const float* scales, const uint8_t* zeros, int64_t group,
                                     const uint16_t* out, int64_t ld_out, int64_t M, int64_t N,
-                                    int64_t K) {
+                                    int64_t K, const void* workspace, size_t ws_bytes) {
   if (!group_ok(group)) return FP8_ERR_BLOCK;
-  if (!weight_shape(N, K) || N == 0 || M < 0 || M >= kMaxDim) return FP8_ERR_SHAPE;
-  if (M > kMaxElems / K || M > kMaxElems / N) return FP8_ERR_SHAPE;
+  if (!product_shape(M, N, K)) return FP8_ERR_SHAPE;
   if (M > 0 && fp8k::int4_linear_items(M, N, K) >= fp8k::kMaxGridItems) return FP8_ERR_SHAPE;
   if (M == 0) return FP8_OK;
   if (!x || !codes || !scales || !out) return FP8_ERR_NULL;
@@ -280,14 +285,25 @@ fp8_status fp8_validate_int4_linear(const uint16_t* x, int64_t ld_x, const uint8
                        vec(scales, N * (K / group), 4), vec(zeros, N * (K / group), 1)};
   for (const Range& r : ins)
     if (overlap(o, r)) return FP8_ERR_ALIAS;
-  return FP8_OK;
+  if (!workspace) return FP8_OK;
+  if (!aligned(workspace, 16)) return FP8_ERR_WORKSPACE;
+  const Range ws = {(uintptr_t)workspace, (uintptr_t)workspace + ws_bytes};
+  for (const Range& r : ins)
+    if (overlap(ws, r)) return FP8_ERR_ALIAS;
+  return overlap(ws, o) ? FP8_ERR_ALIAS : FP8_OK;
+}
+
+size_t fp8_int4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || !product_shape(M, N, K)) return 0;
+  return fp8k::int4_workspace(M, N, K);
 }
 
 fp8_status fp8_int4_linear(const uint16_t* x, int64_t ld_x, const uint8_t* codes,
                            const float* scales, const uint8_t* zeros, int64_t group, uint16_t* out,
-                           int64_t ld_out, int64_t M, int64_t N, int64_t K, void* stream) {
+                           int64_t ld_out, int64_t M, int64_t N, int64_t K, void* workspace,
+                           size_t ws_bytes, void* stream) {
   fp8_status st = fp8_validate_int4_linear(x, ld_x, codes, scales, zeros, group, out, ld_out, M, N,
-                                           K);
+                                           K, workspace, ws_bytes);
   if (st != FP8_OK || M == 0) return st;
   if ((st = check_device()) != FP8_OK) return st;
   fp8k::Int4Args a = {};
@@ -301,6 +317,8 @@ fp8_status fp8_int4_linear(const uint16_t* x, int64_t ld_x, const uint8_t* codes
   a.M = M;
   a.N = N;
   a.K = (int32_t)K;
+  const size_t need = fp8k::int4_workspace(M, N, K);
+  a.parts = workspace && need > 0 && ws_bytes >= need ? (float*)workspace : nullptr;
   return launched(fp8k::launch_int4_linear(a, (int)group, (hipStream_t)stream));
 }
 

@@ -43,7 +43,10 @@ struct Int4Args {
   int64_t ld_out;
   int64_t M, N;
   int32_t K;
+  float* parts;                 // [runs][M][N], or null: one run of K
 };
+// workspace bytes with which K is cut into runs (0: it is not)
+size_t int4_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int4_linear(const Int4Args& a, int group, hipStream_t st);
 uint64_t int4_linear_items(int64_t M, int64_t N, int64_t K);
 

@@ -119,6 +119,11 @@ fp8_status fp8_int4_quant_weight(const uint16_t* w, int64_t ld_w, uint8_t* codes
                                  uint8_t* zeros, int64_t N, int64_t K, int64_t group,
                                  void* stream);
 
+/* Bytes of workspace with which fp8_int4_linear cuts K into runs (0: it does
+ * not; nonzero where more than 4 rows of x have too few tiles of the weight for
+ * all compute units). */
+size_t fp8_int4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
 /* fp8_int4_linear -- out = x . W^T with 4-bit weights.
  *   x      [M, K] bf16, ld_x elements per row                              (input)
  *   codes  [N, K / 2] packed, contiguous                                   (input)
@@ -131,13 +136,20 @@ fp8_status fp8_int4_quant_weight(const uint16_t* w, int64_t ld_w, uint8_t* codes
  * of a group are fp32, 16 + zero times the group's sum of x is taken off in
  * fp32, and the scaled groups are summed in fp32.  Nothing is rounded below
  * that but the result.  A row of x that holds an infinity or a NaN gives NaN.
- * group 32, 64 or 128; K a positive multiple of 128; any N >= 1 and M >= 0
- * (M = 0 does nothing); x, codes and scales 16-byte aligned, out 2-byte aligned,
+ * group 32, 64 or 128; K a positive multiple of 128 below 2^24; any N >= 1 and
+ * M >= 0 (M = 0 does nothing); x, codes and scales 16-byte aligned, out 2-byte aligned,
  * ld_x a multiple of 8, ld_out any >= N.  Zeros above 15 are taken as they are.
- * No workspace. */
+ * workspace (optional, may be NULL): with at least fp8_int4_workspace_bytes(M,
+ * N, K) bytes (16-byte aligned, apart from every tensor of the call, contents
+ * not needed and not read afterwards; calls that can overlap need one each) the
+ * runs of K that it counts are summed in fp32 by workgroups of their own and
+ * then added, in order: the same arithmetic, so results can differ from the
+ * uncut call's in the last bits.  A smaller or NULL workspace runs the call
+ * uncut. */
 fp8_status fp8_int4_linear(const uint16_t* x, int64_t ld_x, const uint8_t* codes,
                            const float* scales, const uint8_t* zeros, int64_t group, uint16_t* out,
-                           int64_t ld_out, int64_t M, int64_t N, int64_t K, void* stream);
+                           int64_t ld_out, int64_t M, int64_t N, int64_t K, void* workspace,
+                           size_t ws_bytes, void* stream);
 
 /* Types of logits. */
 enum { FP8_LOGITS_BF16 = 0, FP8_LOGITS_F32 = 1 };
@@ -201,7 +213,7 @@ fp8_status fp8_validate_int4_quant_weight(const uint16_t* w, int64_t ld_w, const
 fp8_status fp8_validate_int4_linear(const uint16_t* x, int64_t ld_x, const uint8_t* codes,
                                     const float* scales, const uint8_t* zeros, int64_t group,
                                     const uint16_t* out, int64_t ld_out, int64_t M, int64_t N,
-                                    int64_t K);
+                                    int64_t K, const void* workspace, size_t ws_bytes);
 fp8_status fp8_validate_token_logprobs(const void* logits, int logits_type, int64_t ld,
                                        const int64_t* tokens, float scale, int64_t T, int64_t V,
                                        int64_t k, const float* logprobs, const int32_t* ranks,

@@ -42,7 +42,7 @@ def test_exports_and_argument_types():
     c_of = {"int64_t": ctypes.c_int64, "int": ctypes.c_int, "size_t": ctypes.c_size_t,
             "float": ctypes.c_float, "fp8_status": ctypes.c_int}
     sigs, lib = signatures(), _step.lib()
-    assert sorted(sigs) == sorted(_step._SIGS) and len(sigs) == 13
+    assert sorted(sigs) == sorted(_step._SIGS) and len(sigs) == 14
     for name, (ret, params) in sigs.items():
         assert hasattr(lib, name)
         b_ret, b_args = _step._SIGS[name]
@@ -149,8 +149,9 @@ def test_int4_weight_arguments():
     assert quant(z=A[2] + 47) == ALIAS and quant(z=A[2] + 48) == OK and quant(s=A[0]) == ALIAS
 
 
-def int4(x=A[0], ld_x=256, c=A[1], s=A[2], z=A[3], g=64, out=A[4], ld_o=100, M=5, N=100, K=256):
-    return _step.lib().fp8_validate_int4_linear(x, ld_x, c, s, z, g, out, ld_o, M, N, K)
+def int4(x=A[0], ld_x=256, c=A[1], s=A[2], z=A[3], g=64, out=A[4], ld_o=100, M=5, N=100, K=256,
+         ws=None, n=0):
+    return _step.lib().fp8_validate_int4_linear(x, ld_x, c, s, z, g, out, ld_o, M, N, K, ws, n)
 
 
 def test_int4_linear_arguments():
@@ -159,7 +160,7 @@ def test_int4_linear_arguments():
     for g in (0, 16, 256):
         assert int4(g=g) == BLOCK
     for bad in (dict(M=-1), dict(N=0), dict(N=-1), dict(K=0), dict(K=192), dict(M=1 << 31),
-                dict(M=1 << 30, N=1 << 20, ld_o=1 << 20)):
+                dict(K=1 << 24, ld_x=1 << 24), dict(M=1 << 30, N=1 << 20, ld_o=1 << 20)):
         assert int4(**bad) == SHAPE, bad
     for name in ("x", "c", "s", "out"):
         assert int4(**{name: None}) == NULL, name
@@ -169,6 +170,25 @@ def test_int4_linear_arguments():
         assert int4(**{name: A[5] + 8}) == ALIGN, name
     assert int4(out=A[3] + 398) == ALIAS and int4(out=A[3] + 400) == OK
     assert int4(out=A[0]) == ALIAS and int4(out=A[2] + 1598) == ALIAS
+    assert int4(ws=A[6], n=64) == OK and int4(ws=A[6] + 8, n=64) == WORKSPACE
+    assert int4(ws=A[4] + 992, n=64) == ALIAS and int4(ws=A[0] - 16, n=32) == ALIAS
+    assert int4(ws=A[0] - 32, n=32) == OK
+
+
+def test_int4_workspace_sizes():
+    def size(M, N, K):
+        return _step.lib().fp8_int4_workspace_bytes(M, N, K)
+
+    for bad in ((0, 256, 256), (-1, 256, 256), (5, 0, 256), (5, 256, 200), (5, 256, 1 << 24)):
+        assert size(*bad) == 0
+    assert size(1, 256, 4096) == 0 and size(4, 4096, 14336) == 0    # the waves of a workgroup share K
+    assert size(16, 128000, 4096) == 0 and size(16, 256, 4096) == 0
+    n = size(16, 4096, 14336)                                       # x would be read 256 times
+    assert n > 0 and n % (16 * 4096 * 4) == 0 and n // (16 * 4096 * 4) <= 14
+    assert size(64, 65536, 4096) == 0                               # tiles for every compute unit
+    assert size(64, 256, 384) == 0                                  # less than 2 runs of 4 blocks
+    n = size(64, 256, 4096)
+    assert n > 0 and n // (64 * 256 * 4) <= 8
 
 
 def probs(x=A[0], kind=0, ld=1000, tok=A[1], scale=1.0, T=5, V=1000, k=3, lp=A[2], r=A[3], e=A[4],
