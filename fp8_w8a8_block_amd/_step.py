@@ -4,9 +4,14 @@ conventions of _lib and _attention.
 
 No call synchronizes or needs a value on the host, so all of them can be
 captured in a graph with the buffers that they are given.
+
+Calls with arguments as they should be are made whole by _tensor_args
+(csrc/tensor_args.cpp); the checks written out here say what is wrong with the
+others.
 """
 
 import ctypes
+import functools
 
 import torch
 
@@ -61,6 +66,19 @@ def lib():
     return _bound
 
 
+@functools.lru_cache(maxsize=None)
+def _address(name):
+    """Address of a function of the library."""
+    return ctypes.cast(getattr(lib(), name), _vp).value
+
+
+def _stream_here(device):
+    """The stream to call on if this GPU is the current device, else None."""
+    if device.type == "cuda" and torch._C._cuda_getDevice() == device.index:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
+
+
 def _rows(t, name, dtype, device, shape=None):
     """A 2-D device tensor with unit column stride -> (pointer, rows, columns, ld)."""
     got = _attention._tensor_args.rows(t, dtype, device)
@@ -75,6 +93,25 @@ def _rows(t, name, dtype, device, shape=None):
 def _norm(x, weight, residual, eps, mode, scale, out, q, scales, residual_out):
     """Both norms; mode None: no codes."""
     dev = _device_of(x, "x")
+    stream = _stream_here(dev)
+    if stream is not None and x.dim() == 2 and (mode == SCALE_TENSOR) == (scale is not None) and \
+            (residual is not None or residual_out is None) and \
+            not (mode == SCALE_TENSOR and scales is not None):
+        if mode is not None:
+            T, H = x.shape
+            if q is None:
+                q = torch.empty((T, H), dtype=torch.uint8, device=dev)
+            if scales is None and mode != SCALE_TENSOR:
+                scales = torch.empty((T, H // 128) if mode == SCALE_BLOCK else (T,),
+                                     dtype=torch.float32, device=dev)
+        st = _attention._tensor_args.add_rms_norm(
+            _address("fp8_add_rms_norm_quant"), x, residual,
+            residual if residual_out is None else residual_out, weight, eps, out, q, scales,
+            0 if mode is None else mode, scale, dev, stream)
+        if st is not None:
+            if st:
+                _check(st)
+            return q, scale if mode == SCALE_TENSOR else scales
     xp, T, H, ld_x = _rows(x, "x", torch.bfloat16, dev)
     rp, ld_r, rop, ld_ro = None, 0, None, 0
     if residual is not None:
@@ -150,6 +187,18 @@ def qk_norm_mrope_cache(query, key, value, q_weight, k_weight, cos_sin, position
     pairs left, else to the first.  Tokens with a position outside the table
     on any axis are padding."""
     dev = _device_of(query, "query")
+    stream = _stream_here(dev)
+    if stream is not None:
+        if query_out is None:
+            query_out = torch.empty(query.shape, dtype=torch.bfloat16, device=dev)
+        st = _attention._tensor_args.qk_norm_mrope_cache(
+            _address("fp8_qk_norm_mrope_cache"), query, key, value, q_weight, k_weight, eps, cos_sin,
+            bool(interleaved), positions, tuple(sections), bool(in_turn), slot_mapping, query_out,
+            key_cache, value_cache, k_scale, v_scale, dev, stream)
+        if st is not None:
+            if st:
+                _check(st)
+            return query_out
     q, T, Hq, D, ld_q = _heads(query, "query", dev)
     k, Tk, Hk, Dk, ld_k = _heads(key, "key", dev)
     v, Tv, Hv, Dv, ld_v = _heads(value, "value", dev)
@@ -207,7 +256,12 @@ def int4_quant_weight(w, group=128, symmetric=False):
 
 def int4_workspace_bytes(M, N, K):
     """Workspace bytes with which int4_linear cuts K into runs (0: it does not)."""
-    return int(lib().fp8_int4_workspace_bytes(int(M), int(N), int(K)))
+    return _int4_workspace(int(M), int(N), int(K))
+
+
+@functools.lru_cache(maxsize=4096)
+def _int4_workspace(M, N, K):
+    return int(lib().fp8_int4_workspace_bytes(M, N, K))
 
 
 def int4_linear(x, codes, scales, zeros=None, out=None, workspace=None):
@@ -216,6 +270,21 @@ def int4_linear(x, codes, scales, zeros=None, out=None, workspace=None):
     -> bf16 [M, N].  Sizes that cut K into runs (int4_workspace_bytes > 0) get a
     workspace, allocated here unless given."""
     dev = _device_of(x, "x")
+    stream = _stream_here(dev)
+    if stream is not None and x.dim() == 2 and isinstance(codes, torch.Tensor) and codes.dim() == 2:
+        M, N, ws = x.shape[0], codes.shape[0], workspace
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        if ws is None and M > 4:
+            n = _int4_workspace(M, N, x.shape[1])
+            if n:
+                ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        st = _attention._tensor_args.int4_linear(_address("fp8_int4_linear"), x, codes, scales, zeros, out,
+                                                 ws, dev, stream)
+        if st is not None:
+            if st:
+                _check(st)
+            return out
     xp, M, K, ld_x = _rows(x, "x", torch.bfloat16, dev)
     cp, N, half = _matrix(codes, "codes", torch.uint8, dev)
     sp, Ns, groups = _matrix(scales, "scales", torch.float32, dev)
@@ -246,7 +315,12 @@ def int4_linear(x, codes, scales, zeros=None, out=None, workspace=None):
 
 def logprobs_workspace_bytes(T, V, k=0, dtype=torch.bfloat16):
     """Workspace bytes of token_logprobs for logits [T, V] of this type."""
-    return int(lib().fp8_logprobs_workspace_bytes(_logits_type(dtype), int(T), int(V), int(k)))
+    return _logprobs_workspace(_logits_type(dtype), int(T), int(V), int(k))
+
+
+@functools.lru_cache(maxsize=4096)
+def _logprobs_workspace(kind, T, V, k):
+    return int(lib().fp8_logprobs_workspace_bytes(kind, T, V, k))
 
 
 def _logits_type(dtype):
@@ -268,8 +342,9 @@ def token_logprobs(logits, tokens, k=0, scale=1.0, logprobs=None, ranks=None, en
     a NaN or +inf gives NaN and -1.  k is at most 64."""
     dev = _device_of(logits, "logits")
     kind = _logits_type(logits.dtype)
-    p, T, V, ld = _rows(logits, "logits", logits.dtype, dev)
-    k = int(k)
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D with unit column stride")
+    (T, V), k = logits.shape, int(k)
     if k < 0 or k > MAX_TOP or k > V:
         raise ValueError(f"k must be 0 .. {min(V, MAX_TOP)}, got {k}")
     f32, i32 = torch.float32, torch.int32
@@ -285,23 +360,28 @@ def token_logprobs(logits, tokens, k=0, scale=1.0, logprobs=None, ranks=None, en
         top_logprobs = torch.empty((T, k), dtype=f32, device=dev)
     if top_ids is None:
         top_ids = torch.empty((T, k), dtype=i32, device=dev)
+    if workspace is None:
+        n = _logprobs_workspace(kind, T, V, k)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    stream = _stream_here(dev)
+    if stream is not None:
+        st = _attention._tensor_args.token_logprobs(
+            _address("fp8_token_logprobs"), logits, tokens, scale, k, logprobs, ranks, entropy, lse,
+            top_logprobs, top_ids, workspace, dev, stream)
+        if st is not None:
+            if st:
+                _check(st)
+            return logprobs, ranks, entropy, lse, top_logprobs, top_ids
+    p, T, V, ld = _rows(logits, "logits", logits.dtype, dev)
     top = _matrix(top_logprobs, "top_logprobs", f32, dev)
     ids = _matrix(top_ids, "top_ids", i32, dev)
     if top[1:] != (T, k) or ids[1:] != (T, k):
         raise ValueError(f"top_logprobs and top_ids must be [{T}, {k}]")
+    ws_ptr, ws_len = _workspace(workspace, dev)
     args = (p, kind, ld, _vector(tokens, "tokens", torch.int64, dev, T), float(scale), T, V, k,
             _vector(logprobs, "logprobs", f32, dev, T), _vector(ranks, "ranks", i32, dev, T),
             _vector(entropy, "entropy", f32, dev, T), _vector(lse, "lse", f32, dev, T),
-            top[0], ids[0])
-
-    def call():
-        l, ws = lib(), workspace
-        if ws is None:
-            n = l.fp8_logprobs_workspace_bytes(kind, T, V, k)
-            if n:
-                ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        ws_ptr, ws_len = _workspace(ws, dev)
-        return l.fp8_token_logprobs(*args, ws_ptr, ws_len, _raw_stream(dev))
-
-    _check(_call(dev, call))
+            top[0], ids[0], ws_ptr, ws_len)
+    _check(_call(dev, lambda: lib().fp8_token_logprobs(*args, _raw_stream(dev))))
     return logprobs, ranks, entropy, lse, top_logprobs, top_ids

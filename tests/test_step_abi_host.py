@@ -241,3 +241,25 @@ def test_binding_refuses_before_the_library():
         fp8.token_logprobs(x, w)
     with pytest.raises(TypeError):
         fp8.token_logprobs(None, w)
+
+
+def test_whole_calls_refuse_what_is_no_gpu_tensor():
+    from fp8_w8a8_block_amd import _attention
+    import fp8_w8a8_block_amd as fp8
+    fp8.lib()
+    calls, gpu = _attention._tensor_args, torch.device("cuda", 0)      # a name; no GPU is needed here
+    x = torch.zeros((2, 128), dtype=torch.bfloat16)
+    for t in (x, None, 3):
+        assert calls.int4_linear(0, t, t, t, None, t, None, gpu, 0) is None
+        assert calls.add_rms_norm(0, t, None, None, t, 1e-6, t, None, None, 0, None, gpu, 0) is None
+        assert calls.qk_norm_mrope_cache(0, *[t] * 5, 1e-6, t, 0, t, (1, 2), 0, *[t] * 6, gpu, 0) is None
+        assert calls.token_logprobs(0, t, t, 1.0, 0, *[t] * 6, None, gpu, 0) is None
+    for name, n in (("int4_linear", 9), ("add_rms_norm", 13), ("qk_norm_mrope_cache", 20),
+                    ("token_logprobs", 14)):
+        for wrong in (0, n - 1, n + 1):
+            with pytest.raises(TypeError):
+                getattr(calls, name)(*[None] * wrong)
+    with pytest.raises(TypeError):
+        calls.add_rms_norm(0, x, None, None, x, "eps", x, None, None, 0, None, gpu, 0)
+    with pytest.raises(TypeError):
+        calls.qk_norm_mrope_cache(0, *[x] * 5, 1e-6, x, 0, x, ("a",), 0, *[x] * 6, gpu, 0)
