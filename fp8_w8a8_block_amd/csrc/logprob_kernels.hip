@@ -59,6 +59,35 @@ __device__ __forceinline__ void join(Stats& a, float m, float s, float d, float 
   a.d += d;
 }
 
+// f over the wave's 64 values, in every lane
+template <typename F>
+__device__ __forceinline__ float wave_fold(float v, F f) {
+  auto other = [](float x, auto ctrl) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+        0, (int)__float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  v = f(v, other(v, std::integral_constant<int, 0x128>()));     // the row of 16 turned by 8, 4, 2, 1
+  v = f(v, other(v, std::integral_constant<int, 0x124>()));
+  v = f(v, other(v, std::integral_constant<int, 0x122>()));
+  v = f(v, other(v, std::integral_constant<int, 0x121>()));
+  auto row = [&](int lane) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+  };
+  return f(f(row(0), row(16)), f(row(32), row(48)));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return wave_fold(v, [](float a, float b) { return a + b; });
+}
+
+// the wave's sums, in every lane (above is not touched)
+__device__ __forceinline__ void join_wave(Stats& a, float c) {
+  const float m = wave_fold(a.m, [](float x, float y) { return __builtin_fmaxf(x, y); });
+  rebase(a.m, m, c, a.s, a.d);
+  a.m = m;
+  a.s = wave_sum(a.s);
+  a.d = wave_sum(a.d);
+}
+
 // A row as vectors of 16 bytes from the 128-byte line on in which it starts:
 // vector v, value e is logit v V + e - lead.
 template <bool kF32>
@@ -118,10 +147,11 @@ __device__ __forceinline__ float segment_max(float v) {
   return __builtin_fmaxf(v, other(v, std::integral_constant<int, 0x141>())); // 7 - lane of 8
 }
 
-// One batch of U vectors a thread, kThreads apart: x is theirs.
+// One batch of U vectors a thread, kThreads apart: x is theirs.  `segments` of the
+// batch are the part's.
 template <bool kF32, int U>
 __device__ __forceinline__ void take(const float (&x)[U][Row<kF32>::V], float c, float mine,
-                                     Stats& a, float* maxima) {
+                                     Stats& a, float* maxima, uint32_t segments) {
   constexpr int V = Row<kF32>::V;
   float top[U], m = a.m;
 #pragma unroll
@@ -145,47 +175,85 @@ __device__ __forceinline__ void take(const float (&x)[U][Row<kF32>::V], float c,
       a.above += (uint32_t)__builtin_popcountll(__ballot(x[u][e] > mine));
     }
     const float seg = segment_max(top[u]);
-    if ((threadIdx.x & 7u) == 0) maxima[u * kSweep + (threadIdx.x >> 3)] = seg;
+    const uint32_t at = u * kSweep + (threadIdx.x >> 3);
+    if ((threadIdx.x & 7u) == 0 && at < segments) maxima[at] = seg;
   }
 }
 
+// A batch that may reach beyond the row or the part: every load is on its way before
+// any is looked at, the vectors at the ends of the row (and there is none but those
+// if it is short) are read value by value.
+template <bool kF32, int U>
+__device__ __forceinline__ void load_batch(const Row<kF32>& row, uint32_t seg, uint4 (&r)[U]) {
+  constexpr int V = Row<kF32>::V;
+  const uint32_t lo = (row.lead + V - 1) / V, hi = (row.lead + row.n) / V;    // whole: lo .. hi - 1
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint32_t v = seg * 8u + threadIdx.x + u * kThreads;
+    v = v < lo ? lo : v;
+    v = v < hi ? v : hi - 1;
+    r[u] = lo < hi ? row.base[v] : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+template <bool kF32, int U>
+__device__ __forceinline__ void take_edge(const Row<kF32>& row, const uint4 (&r)[U], uint32_t seg,
+                                          uint32_t last, float c, float mine, Stats& a,
+                                          float* maxima) {
+  constexpr int V = Row<kF32>::V;
+  const uint32_t lo = (row.lead + V - 1) / V, hi = (row.lead + row.n) / V, end = last * 8u;
+  float x[U][V];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t v = seg * 8u + threadIdx.x + u * kThreads;
+    row.unpack(r[u], x[u]);
+    if (v < lo || v >= hi || v >= end) {
+      if (v < end) {
+        row.load(v, x[u]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[u][e] = -kInf;
+      }
+    }
+  }
+  take<kF32, U>(x, c, mine, a, maxima, last - seg);
+}
+
 // Segments first .. last - 1 of a row, their maxima to maxima[0 ..]; the sums of
-// the whole workgroup in every thread.
-template <bool kF32>
-__device__ Stats stream(const Row<kF32>& row, uint32_t first, uint32_t last, float c, float mine,
-                        float* maxima) {
+// the whole workgroup in every thread.  get_mine reads the token's logit, once the
+// first loads of the row are on their way.
+template <bool kF32, typename F>
+__device__ Stats stream(const Row<kF32>& row, uint32_t first, uint32_t last, float c, float& mine,
+                        float* maxima, F get_mine) {
   constexpr int V = Row<kF32>::V, U = 4;
   __shared__ Stats shared[kThreads / 64];
   Stats a = {-kInf, 0.0f, 0.0f, 0u};
-  uint32_t seg = first;
-  while (seg < last) {
-    const uint32_t v = seg * 8u + threadIdx.x;
-    // all of the batch inside the row, for all threads alike
+  mine = kInf;
+  for (uint32_t seg = first; seg < last; seg += U * kSweep) {
+    float* to = maxima + (seg - first);
+    // all of the batch inside the row and the part, for all threads alike
     if (seg + U * kSweep <= last && row.whole(seg * 8u) &&
         row.whole((seg + U * kSweep) * 8u - 1u)) {
       uint4 r[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) r[u] = row.base[v + u * kThreads];
+      for (int u = 0; u < U; ++u) r[u] = row.base[seg * 8u + threadIdx.x + u * kThreads];
+      if (seg == first) mine = get_mine();
       float x[U][V];
 #pragma unroll
       for (int u = 0; u < U; ++u) row.unpack(r[u], x[u]);
-      take<kF32, U>(x, c, mine, a, maxima + (seg - first));
-      seg += U * kSweep;
+      take<kF32, U>(x, c, mine, a, to, U * kSweep);
+    } else if (last - seg > 2 * kSweep) {
+      uint4 r[U];
+      load_batch<kF32, U>(row, seg, r);
+      if (seg == first) mine = get_mine();
+      take_edge<kF32, U>(row, r, seg, last, c, mine, a, to);
     } else {
-      // one vector a thread; behind the last segment there is nothing to take
-      float x[1][V];
-      if (seg + (threadIdx.x >> 3) < last) {
-        row.load(v, x[0]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) x[0][e] = -kInf;
-      }
-      take<kF32, 1>(x, c, mine, a, maxima + (seg - first));
-      seg += kSweep;
+      uint4 r[2];
+      load_batch<kF32, 2>(row, seg, r);
+      if (seg == first) mine = get_mine();
+      take_edge<kF32, 2>(row, r, seg, last, c, mine, a, to);
     }
   }
-  for (int i = 1; i < 64; i <<= 1)
-    join(a, __shfl_xor(a.m, i), __shfl_xor(a.s, i), __shfl_xor(a.d, i), c);
+  join_wave(a, c);
   if ((threadIdx.x & 63u) == 0) shared[threadIdx.x >> 6] = a;
   __syncthreads();
   Stats all = shared[0];
@@ -203,33 +271,71 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
+// a logit and its place as one number: of equal logits the lower index is the larger
+__device__ __forceinline__ uint64_t rank_key(float x, uint32_t index) {
+  return (uint64_t)order_key(x) << 32 | (0xffffffffu - index);
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float(key ^ (key & 0x80000000u ? 0x80000000u : 0xffffffffu));
+}
+
 struct Select {
+  uint64_t key[kMaxRanked];
   float super[kThreads];
   uint32_t listed[kMaxListed];
-  float value[kMaxRanked];
-  uint32_t index[kMaxRanked];
   uint32_t hist[256];
   uint32_t wave[kThreads / 64];
   uint32_t segments, ranked, bin, left;
   float bound;
+  Stats all;
 };
 
-// Largest key that at least k of the 512 values reach (or a key between it and
-// the next lower one that exactly k reach); one wave, k <= 512.
-__device__ __forceinline__ uint32_t kth_key(const float* v, uint32_t k) {
-  uint32_t key[kThreads / 64], found = 0u;
+// Largest key that at least k of the wave's 64 N values reach (or one between it and
+// the next lower value that exactly k reach), k <= 64 N.
+template <int N>
+__device__ __forceinline__ uint32_t kth_key(const float (&v)[N], uint32_t k) {
+  uint32_t key[N], found = 0u;
 #pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) key[i] = order_key(v[i * 64 + (threadIdx.x & 63u)]);
+  for (int i = 0; i < N; ++i) key[i] = order_key(v[i]);
   for (int bit = 31; bit >= 0; --bit) {
     const uint32_t t = found | (1u << bit);
     uint32_t n = 0u;
 #pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i)
-      n += (uint32_t)__builtin_popcountll(__ballot(key[i] >= t));
+    for (int i = 0; i < N; ++i) n += (uint32_t)__builtin_popcountll(__ballot(key[i] >= t));
     if (n >= k) found = t;
     if (n == k) break;
   }
   return found;
+}
+
+// Step 1 of the selection: sh.bound, which k logits at least reach.  Thread t holds the
+// maximum of segments t, t + 512, ... (neighbouring ones apart, so that a cluster
+// of likely tokens does not share a maximum); the k-th largest of these maxima is a
+// bound, and for k up to 32 that of 64 of them, at a third of the time: it lets 24
+// logits pass for k = 20 where 512 let 20 pass.  `aside` is done by the second wave
+// meanwhile.  Ends with a barrier.
+template <typename F>
+__device__ __forceinline__ void bound_top(const float* maxima, uint32_t segments, uint32_t k,
+                                          Select& sh, F aside) {
+  const uint32_t tid = threadIdx.x;
+  float m = -kInf;
+  for (uint32_t s = tid; s < segments; s += kThreads) m = __builtin_fmaxf(m, maxima[s]);
+  sh.super[tid] = m;
+  if (tid == 0) sh.segments = sh.ranked = 0u;
+  __syncthreads();
+  if (tid < 64) {
+    float v[kThreads / 64], one[1] = {-kInf};
+#pragma unroll
+    for (int i = 0; i < kThreads / 64; ++i) {
+      v[i] = sh.super[i * 64 + tid];
+      one[0] = __builtin_fmaxf(one[0], v[i]);
+    }
+    const float f = key_value(k <= 32 ? kth_key(one, k) : kth_key(v, k));
+    if (tid == 0) sh.bound = f == f ? f : -kInf;    // below -inf in the order: no bound
+  } else if (tid < 128) {
+    aside();
+  }
+  __syncthreads();
 }
 
 // f(value, index) for every logit of the row, in any order
@@ -246,45 +352,26 @@ __device__ __forceinline__ void each_logit(const Row<kF32>& row, F f) {
   }
 }
 
-// The k most likely logits of a row, by falling value and rising index.  `log_p`
-// turns a logit into what is written.
+// Step 2: the k most likely logits of a row, by falling value and rising index.
+// `log_p` turns a logit into what is written.
 template <bool kF32, typename F>
 __device__ void select_top(const Row<kF32>& row, const float* maxima, uint32_t segments, uint32_t k,
                            float* top, int32_t* ids, Select& sh, F log_p) {
   constexpr int V = Row<kF32>::V;
   const uint32_t tid = threadIdx.x;
-  const uint32_t per = (segments + kThreads - 1) / kThreads;
-  const uint32_t s0 = tid * per, s1 = s0 + per < segments ? s0 + per : segments;
-  float m = -kInf;
-  for (uint32_t s = s0; s < s1; ++s) m = __builtin_fmaxf(m, maxima[s]);
-  sh.super[tid] = m;
-  if (tid == 0) sh.segments = sh.ranked = 0u;
-  __syncthreads();
-  if (tid < 64) {
-    const uint32_t key = kth_key(sh.super, k);
-    if (tid == 0) {
-      const float f = __uint_as_float(key ^ (key & 0x80000000u ? 0x80000000u : 0xffffffffu));
-      sh.bound = f == f ? f : -kInf;                // below -inf in the order: no bound
-    }
-  }
-  __syncthreads();
   const float bound = sh.bound;
   // masked logits are not listed: the lowest of them are filled in below
   auto passes = [&](float x) { return x >= bound && x > -kInf; };
-  if (passes(m))
-    for (uint32_t s = s0; s < s1; ++s)
-      if (passes(maxima[s])) {
-        const uint32_t i = atomicAdd(&sh.segments, 1u);
-        if (i < kMaxListed) sh.listed[i] = s;
-      }
+  for (uint32_t s = tid; s < segments; s += kThreads)
+    if (passes(maxima[s])) {
+      const uint32_t i = atomicAdd(&sh.segments, 1u);
+      if (i < kMaxListed) sh.listed[i] = s;
+    }
   __syncthreads();
   const uint32_t listed = sh.segments;
   auto rank_this = [&](float x, uint32_t index) {
     const uint32_t i = atomicAdd(&sh.ranked, 1u);
-    if (i < kMaxRanked) {
-      sh.value[i] = x;
-      sh.index[i] = index;
-    }
+    if (i < kMaxRanked) sh.key[i] = rank_key(x, index);
   };
   if (listed <= kMaxListed) {
     for (uint32_t i = tid >> 3; i < listed; i += kSweep) {
@@ -352,17 +439,16 @@ __device__ void select_top(const Row<kF32>& row, const float* maxima, uint32_t s
     __syncthreads();
     ranked = sh.ranked;                             // k - left
   }
-  for (uint32_t i = tid; i < ranked; i += kThreads) {
-    const float x = sh.value[i];
-    const uint32_t index = sh.index[i];
+  // eight at a time, so that their reads overlap: LDS beyond the last holds what it may
+  if (tid < ranked) {
+    const uint64_t mine = sh.key[tid];
     uint32_t rank = 0u;
-    for (uint32_t j = 0; j < ranked; ++j) {
-      const float y = sh.value[j];
-      rank += y > x || (y == x && sh.index[j] < index);
-    }
+    for (uint32_t j = 0; j < ranked; j += 8u)
+#pragma unroll
+      for (uint32_t e = 0; e < 8; ++e) rank += j + e < ranked && sh.key[j + e] > mine;
     if (rank < k) {
-      top[rank] = log_p(x);
-      ids[rank] = (int32_t)index;
+      top[rank] = log_p(key_value((uint32_t)(mine >> 32)));
+      ids[rank] = (int32_t)(0xffffffffu - (uint32_t)mine);
     }
   }
   // the first logits of key `equal`, by index
@@ -400,10 +486,12 @@ __device__ void select_top(const Row<kF32>& row, const float* maxima, uint32_t s
   }
 }
 
-// A row's outputs from its sums.
-template <bool kF32>
-__device__ void finish(const LogprobArgs& a, int64_t t, const Row<kF32>& row, const Stats& all,
-                       bool given, float mine, const float* maxima, uint32_t segments, Select& sh) {
+// A row's outputs.  Its sums are sh.all once `sums` has been called by the second wave.
+template <bool kF32, typename F>
+__device__ void finish(const LogprobArgs& a, int64_t t, const Row<kF32>& row, float mine,
+                       const float* maxima, uint32_t segments, Select& sh, F sums) {
+  bound_top(maxima, segments, a.k ? (uint32_t)a.k : 1u, sh, sums);
+  const Stats all = sh.all;
   const bool none = all.m == -kInf && all.s == 0.0f;   // nothing but -inf
   const bool good = none || all.s == all.s;            // no NaN, no +inf
   const float from = anchor(all.m), log_s = __builtin_amdgcn_logf(all.s);
@@ -412,6 +500,7 @@ __device__ void finish(const LogprobArgs& a, int64_t t, const Row<kF32>& row, co
     return !good ? nan : x == -kInf ? -kInf : __builtin_fmaf(x - from, a.scale, -log_s * kLn2);
   };
   if (threadIdx.x == 0) {
+    const bool given = a.tokens[t] >= 0 && a.tokens[t] < a.V;
     a.logprobs[t] = given ? log_p(mine) : 0.0f;
     a.ranks[t] = given && good ? (int32_t)all.above : -1;
     a.entropy[t] = !good ? nan : none ? 0.0f : (log_s - all.d / all.s) * kLn2;
@@ -428,13 +517,11 @@ __device__ void finish(const LogprobArgs& a, int64_t t, const Row<kF32>& row, co
   }
 }
 
+// the logit of the row's token; +inf, which nothing is above, if there is none
 template <bool kF32>
-__device__ __forceinline__ bool token_logit(const LogprobArgs& a, int64_t t, const Row<kF32>& row,
-                                            float& mine) {
+__device__ __forceinline__ float token_logit(const LogprobArgs& a, int64_t t, const Row<kF32>& row) {
   const int64_t token = a.tokens[t];
-  const bool given = token >= 0 && token < a.V;
-  mine = given ? row.at((uint32_t)token) : kInf;
-  return given;
+  return token >= 0 && token < a.V ? row.at((uint32_t)token) : kInf;
 }
 
 __device__ __forceinline__ uint32_t segments_of(uint32_t lead, int64_t vocab, int per) {
@@ -450,10 +537,12 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
   const Row<kF32> row(a.logits, a.ld, t, a.V);
   const float c = a.scale * kLog2e;
   float mine;
-  const bool given = token_logit(a, t, row, mine);
   const uint32_t segments = segments_of(row.lead, a.V, 8 * Row<kF32>::V);
-  const Stats all = stream(row, 0u, segments, c, mine, maxima);
-  finish(a, t, row, all, given, mine, maxima, segments, sh);
+  const Stats all = stream(row, 0u, segments, c, mine, maxima,
+                           [&] { return token_logit(a, t, row); });
+  finish(a, t, row, mine, maxima, segments, sh, [&] {
+    if (threadIdx.x == 64) sh.all = all;
+  });
 }
 
 // Few rows: the pass over `parts` parts of each, every one of `share` segments, ...
@@ -465,14 +554,14 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobArgs a, u
   const Row<kF32> row(a.logits, a.ld, t, a.V);
   const float c = a.scale * kLog2e;
   float mine;
-  token_logit(a, t, row, mine);
   const uint32_t segments = segments_of(row.lead, a.V, 8 * Row<kF32>::V);
   const uint32_t first = p * share < segments ? p * share : segments;
   const uint32_t last = first + share < segments ? first + share : segments;
   Stats* stats = reinterpret_cast<Stats*>(a.ws);
   float* maxima = reinterpret_cast<float*>(stats + (uint64_t)a.T * parts) +
                   (uint64_t)blockIdx.x * share;
-  const Stats all = stream(row, first, last, c, mine, maxima);
+  const Stats all = stream(row, first, last, c, mine, maxima,
+                           [&] { return token_logit(a, t, row); });
   if (threadIdx.x == 0) stats[blockIdx.x] = all;
 }
 
@@ -484,23 +573,21 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, u
   const int64_t t = blockIdx.x;
   const Row<kF32> row(a.logits, a.ld, t, a.V);
   const float c = a.scale * kLog2e;
-  float mine;
-  const bool given = token_logit(a, t, row, mine);
+  const float mine = token_logit(a, t, row);
   const Stats* stats = reinterpret_cast<const Stats*>(a.ws) + (uint64_t)t * parts;
-  Stats all = {-kInf, 0.0f, 0.0f, 0u};
-  for (uint32_t p = threadIdx.x & 63u; p < parts; p += 64u) {
-    join(all, stats[p].m, stats[p].s, stats[p].d, c);
-    all.above += stats[p].above;
-  }
-  for (int i = 1; i < 64; i <<= 1) {
-    join(all, __shfl_xor(all.m, i), __shfl_xor(all.s, i), __shfl_xor(all.d, i), c);
-    all.above += __shfl_xor(all.above, i);
-  }
   const float* maxima = reinterpret_cast<const float*>(reinterpret_cast<const Stats*>(a.ws) +
                                                        (uint64_t)a.T * parts) +
                         (uint64_t)t * parts * share;
-  finish(a, t, row, all, given, mine, maxima,
-         segments_of(row.lead, a.V, 8 * Row<kF32>::V), sh);
+  finish(a, t, row, mine, maxima, segments_of(row.lead, a.V, 8 * Row<kF32>::V), sh, [&] {
+    Stats all = {-kInf, 0.0f, 0.0f, 0u};
+    for (uint32_t p = threadIdx.x & 63u; p < parts; p += 64u) {
+      join(all, stats[p].m, stats[p].s, stats[p].d, c);
+      all.above += stats[p].above;
+    }
+    for (int i = 1; i < 64; i <<= 1) all.above += __shfl_xor(all.above, i);
+    join_wave(all, c);
+    if (threadIdx.x == 64) sh.all = all;
+  });
 }
 
 struct Plan {
@@ -508,16 +595,17 @@ struct Plan {
 };
 
 // One workgroup per row where there are rows enough to fill the card (or little to
-// share), and its segment maxima fit LDS.
+// share), and its segment maxima fit LDS.  Fewer rows are cut into parts of two
+// sweeps, or of whole batches of four: about 1024 parts in all.
 Plan plan_of(bool f32, int64_t T, int64_t V) {
   // the row may start anywhere in its first segment
   const int64_t per = f32 ? 32 : 64, segments = (V + 2 * per - 2) / per;
   const int64_t sweeps = (segments + kSweep - 1) / kSweep;
-  int64_t parts = (1024 + T - 1) / T;
-  const int64_t least = (segments + kMaxSegments - 1) / kMaxSegments;
-  if (parts > (sweeps + 1) / 2) parts = (sweeps + 1) / 2;
-  if (parts < least) parts = least;
-  const int64_t share = (sweeps + parts - 1) / parts * kSweep;
+  int64_t each = (sweeps * T + 1023) / 1024;
+  each = each <= 2 ? 2 : (each + 3) / 4 * 4;
+  if (T >= 1024 || each >= sweeps) each = sweeps;
+  if (each > kMaxSegments / kSweep) each = kMaxSegments / kSweep;
+  const int64_t share = each * kSweep;
   return {(uint32_t)((segments + share - 1) / share), (uint32_t)share};
 }
 
