@@ -49,13 +49,11 @@ struct NormRopeArgs {
   int64_t capacity;             // slots of the cache
   const float* k_scale;
   const float* v_scale;
-  // positions of several axes (axes > 0): [axes, T], ld_pos apart.  Pair i belongs
-  // to axis #{b : i >= bound[b]}, b < 3; in turn, to axis i % axes while i <
-  // bound[i % axes], else to axis 0
+  // positions of several axes (axes > 0): [axes, T], ld_pos apart; the axis of each
+  // rotated pair, two bits
   int64_t ld_pos;
   int32_t axes;
-  int32_t bound[4];
-  bool in_turn;
+  uint32_t axis_bits[16];
 };
 hipError_t launch_norm_rope(const NormRopeArgs& a, bool interleaved, hipStream_t st);
 

@@ -26,9 +26,9 @@ namespace {
 // L lanes per head.  `chunks` lane groups share a token's Hq + 2 Hk heads: group
 // j takes heads j, j + chunks, ..., so that a wave's groups read neighbouring
 // heads and are mostly all at queries, at keys or at values.
-// kAxes: positions on several axes.  A lane's 8 pairs (4 where neighbours are
-// paired) may belong to different axes, so it reads their angles one by one,
-// unless the token stands at one position on all axes, as text does.
+// kAxes: positions on several axes.  Lane c reads the angles of pairs 4 c .. 4 c + 3
+// at the positions of all axes that differ, 16 bytes each, keeps each pair's axis',
+// and hands them to the lanes that turn these pairs.
 template <int L, bool kInterleaved, bool kAxes>
 __global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, uint32_t chunks) {
   const uint32_t item = blockIdx.x * (256u / L) + threadIdx.x / L;
@@ -49,17 +49,17 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, uint32_t
   };
   uint4 next = fetch(h0);                           // on its way while the angles are found
   const int64_t pos = a.positions[t], slot = a.slots[t];
-  if (pos < 0 || pos >= a.max_pos) return;
   int64_t at[4] = {pos, pos, pos, pos};
+  bool inside = pos >= 0 && pos < a.max_pos;
   if (kAxes) {
+    // the last axis again for those that are not there: no branch between the loads
 #pragma unroll
-    for (int i = 1; i < 4; ++i)
-      if (i < a.axes) at[i] = a.positions[i * a.ld_pos + t];
-#pragma unroll
-    for (int i = 1; i < 4; ++i)
-      if (at[i] < 0 || at[i] >= a.max_pos) return;
+    for (int i = 1; i < 4; ++i) {
+      at[i] = a.positions[(int64_t)(i < a.axes ? i : a.axes - 1) * a.ld_pos + t];
+      inside &= at[i] >= 0 && at[i] < a.max_pos;
+    }
   }
-  const bool apart = kAxes && (at[1] != pos || at[2] != pos || at[3] != pos);
+  if (!inside) return;
   const bool keep = slot >= 0 && slot < a.capacity;
   const bool turns = c * 8 < a.rot;
   const int half = a.rot / 2;
@@ -71,31 +71,50 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, uint32_t
     cs[e] = 1.0f;
     sn[e] = 0.0f;
   }
-  if (turns && apart) {
-    const bool low = kInterleaved || c * 8 < half;
-    const int j0 = kInterleaved ? c * 4 : low ? c * 8 : c * 8 - half;
-    const uint32_t inv = 65536u / (uint32_t)a.axes + 1u;      // i * inv >> 16 = i / axes, i < 2^8
+  if (kAxes) {
+    // The axes of the lane's pairs, two bits each.  Each word goes through a scalar
+    // register: the compiler makes an index by lane of a plain selection, and that
+    // is a vector load of the launch's arguments, which lie in host memory.
+    uint32_t word = 0;
 #pragma unroll
-    for (int e = 0; e < (kInterleaved ? 4 : 8); ++e) {
-      const int j = j0 + e;
-      int ax;
-      if (a.in_turn) {
-        ax = j - (int)((uint32_t)j * inv >> 16) * a.axes;
-        const int most = ax == 0 ? a.bound[0] : ax == 1 ? a.bound[1]
-                       : ax == 2 ? a.bound[2] : a.bound[3];
-        ax = j < most ? ax : 0;
-      } else {
-        ax = (j >= a.bound[0]) + (j >= a.bound[1]) + (j >= a.bound[2]);
+    for (int i = 0; i < (L + 3) / 4; ++i) {
+      uint32_t w = a.axis_bits[i];
+      asm("" : "+s"(w));
+      word = (c >> 2) == i ? w : word;
+    }
+    const uint32_t bits = word >> ((c & 3) * 8);
+    float vc[4] = {1.0f, 1.0f, 1.0f, 1.0f}, vs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (turns) {                                    // a table of no columns holds nothing
+      float4 rc[4], rs[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* row = a.cos_sin + at[i] * a.rot + c * 4;
+        rc[i] = *reinterpret_cast<const float4*>(row);
+        rs[i] = *reinterpret_cast<const float4*>(row + half);
       }
-      const int64_t p = ax == 0 ? at[0] : ax == 1 ? at[1] : ax == 2 ? at[2] : at[3];
-      const float vc = a.cos_sin[p * a.rot + j], vs = a.cos_sin[p * a.rot + half + j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float ci[4] = {rc[i].x, rc[i].y, rc[i].z, rc[i].w};
+        const float si[4] = {rs[i].x, rs[i].y, rs[i].z, rs[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool its = (bits >> (2 * e) & 3u) == (uint32_t)i;
+          vc[e] = its ? ci[e] : vc[e];
+          vs[e] = its ? si[e] : vs[e];
+        }
+      }
+    }
+    const bool low = c * 8 < half;
+    const int from = (threadIdx.x & 63) - c + (low ? c * 2 : c * 2 - half / 4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
       if (kInterleaved) {
-        cs[2 * e] = cs[2 * e + 1] = vc;
-        sn[2 * e] = -vs;
-        sn[2 * e + 1] = vs;
+        cs[e] = vc[e / 2];
+        sn[e] = (e & 1) ? vs[e / 2] : -vs[e / 2];
       } else {
-        cs[e] = vc;
-        sn[e] = low ? -vs : vs;
+        const float oc = __shfl(vc[e & 3], from + e / 4), os = __shfl(vs[e & 3], from + e / 4);
+        cs[e] = turns ? oc : 1.0f;
+        sn[e] = !turns ? 0.0f : low ? -os : os;
       }
     }
   } else if (turns) {
@@ -187,18 +206,20 @@ int lanes_of(int64_t D) {
 // Heads per lane group: one while the step is small (latency: every head of
 // every token at once), up to six while three waves per SIMD are left, so that
 // a token's angles are read for several heads.  8191 tokens of 48 heads of 128
-// take 50 us with 2, 42.4 with 6, 45.7 with 12.
-int heads_per_group(int64_t T, int heads, int L) {
+// take 50 us with 2, 42.4 with 6, 45.7 with 12.  With several axes, whose angles
+// cost up to four reads and an exchange between lanes, up to twelve: 51.2 us with
+// 4, 48.9 with 6, 45.2 with 12, 46.2 with 24.
+int heads_per_group(int64_t T, int heads, int L, bool axes) {
   const int64_t lanes = T * heads * L;
-  for (int per : {6, 4, 3, 2})
-    if (lanes / per >= (int64_t)256 * 4 * 3 * 64) return per;
+  for (int per : {12, 6, 4, 3, 2})
+    if ((per <= 6 || axes) && lanes / per >= (int64_t)256 * 4 * 3 * 64) return per;
   return 1;
 }
 
 template <int L>
 void launch_l(const NormRopeArgs& a, bool inter, hipStream_t st) {
   const int heads = a.Hq + 2 * a.Hk;
-  const int per = heads_per_group(a.T, heads, L);
+  const int per = heads_per_group(a.T, heads, L, a.axes > 1);
   const int chunks = (heads + per - 1) / per;
   const int64_t items = a.T * chunks * L;
   const dim3 grid((uint32_t)((items + 255) / 256));
@@ -214,9 +235,10 @@ void launch_l(const NormRopeArgs& a, bool inter, hipStream_t st) {
 
 }  // namespace
 
+// (with one axis: more axes make no more groups)
 uint64_t norm_rope_items(int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
   const int L = lanes_of(D);
-  const int heads = (int)(Hq + 2 * Hk), per = heads_per_group(T, heads, L);
+  const int heads = (int)(Hq + 2 * Hk), per = heads_per_group(T, heads, L, false);
   return ((uint64_t)T * ((heads + per - 1) / per) * L + 255) / 256 * 256;
 }
 

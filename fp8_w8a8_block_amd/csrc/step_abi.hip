@@ -44,7 +44,8 @@ bool product_shape(int64_t M, int64_t N, int64_t K) {
          M <= kMaxElems / K && M <= kMaxElems / N;
 }
 
-// The axes' pairs in the form that the kernel takes; false if they do not fit.
+// The axis of each of `half` pairs in the form that the kernel takes; false if the
+// sections do not fit.
 bool axes_of(int64_t A, const int64_t* sections, int order, int64_t half, fp8k::NormRopeArgs* a) {
   int64_t sum = 0;
   for (int64_t i = 0; i < A; ++i) {
@@ -55,17 +56,16 @@ bool axes_of(int64_t A, const int64_t* sections, int order, int64_t half, fp8k::
       return false;
   }
   if (sum != half) return false;
-  int64_t upto = 0;
-  for (int64_t i = 0; i < 4; ++i) {
+  int64_t axis = 0, end = sections[0];
+  for (int64_t i = 0; i < half; ++i) {
     if (order == FP8_AXES_IN_TURN) {
-      a->bound[i] = i < A ? (int32_t)(A * sections[i]) : 0;
+      axis = i < A * sections[i % A] ? i % A : 0;
     } else {
-      upto += i < A ? sections[i] : 0;
-      a->bound[i] = i + 1 < A ? (int32_t)upto : INT32_MAX;
+      while (i >= end) end += sections[++axis];
     }
+    a->axis_bits[i / 16] |= (uint32_t)axis << (i % 16 * 2);
   }
   a->axes = (int32_t)A;
-  a->in_turn = order == FP8_AXES_IN_TURN;
   return true;
 }
 
