@@ -95,6 +95,14 @@ CASES = {
     "prompt_middle_groups": (257, 272, 1024, 64, False, 0, 0),
     "wide": (3, 20000, 128, 128, False, 0, 0),
     "wider": (5, 70001, 128, 64, True, 0, 0),
+    "few_tall": (4, 40000, 256, 64, True, 0, 0),
+    "some_columns": (9, 6500, 256, 64, True, 0, 0),
+    "more_columns": (6, 9000, 256, 128, False, 0, 0),
+    "runs_of_a_batch": (16, 2048, 16384, 128, True, 0, 0),
+    "runs_odd_columns": (24, 515, 8192, 64, False, 8, 3),
+    "runs_of_a_prompt": (100, 301, 4096, 32, True, 0, 0),
+    "runs_even_columns": (70, 300, 4096, 128, False, 0, 0),
+    "chunks_of_groups": (3, 20001, 40960, 32, True, 0, 0),
     "wider_batch": (20, 66000, 128, 32, True, 0, 0),
 }
 
@@ -132,6 +140,26 @@ def test_each_value_finds_its_weight(M, group):
         assert np.array_equal(out[:len(ks)], want)
         if k0 > 64:
             break
+
+
+@pytest.mark.parametrize("M, N, K", [(24, 515, 8192), (100, 300, 4096)])
+def test_workspaces(M, N, K):
+    """A call without the workspace, or with a part of it, does not cut K."""
+    rng = np.random.default_rng([M, N])
+    c, s, z = weights(rng, N, K, 64, True)
+    x = normal(rng, M, K)
+    d = [dev(x), torch.from_numpy(step.int4_pack_ref(c)).cuda(), torch.from_numpy(s).cuda(),
+         torch.from_numpy(z).cuda()]
+    n = fp8.int4_workspace_bytes(M, N, K)
+    assert n > 0 and fp8.int4_workspace_bytes(1, N, K) == 0
+    store = torch.full((n + 32,), 0x55, dtype=torch.uint8, device="cuda")
+    for size in (n, n - 16, 0):
+        ws = store[16:16 + size]
+        check(fp8.int4_linear(*d, workspace=ws), x, c, s, z)
+        assert (store[:16] == 0x55).all() and (store[16 + size:] == 0x55).all()
+        store.fill_(0x55)
+    with pytest.raises(ValueError):
+        fp8.int4_linear(*d, workspace=store[1:])                   # not aligned
 
 
 def test_rows_of_one_sign():

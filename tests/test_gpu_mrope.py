@@ -102,6 +102,7 @@ CASES = {
     "an_empty_first": (12, 2, 1, 64, 64, (0, 16, 16), False, False, 16),
     "widest": (6, 2, 1, 512, 512, (100, 78, 78), True, False, 16),
     "no_rotation": (9, 2, 1, 64, 0, (0, 0), False, False, 16),
+    "many_heads": (2300, 64, 2, 128, 64, (12, 10, 10), True, False, 16),
     "many": (1700, 8, 2, 128, 128, (24, 20, 20), True, False, 16),
 }
 
