@@ -91,9 +91,11 @@ __global__ __launch_bounds__(256) void int4_quant_kernel(
 // A packed dword as 8 bf16 operand values 16 + c (bits of 16.0: 0x4180; the
 // code's unit is mantissa bit 3)
 __device__ __forceinline__ bf16x8 operand(uint32_t d) {
-  constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u;
-  const uint4 r = make_uint4(((d << 3) & kMask) | kBase, ((d >> 1) & kMask) | kBase,
-                             ((d >> 5) & kMask) | kBase, ((d >> 9) & kMask) | kBase);
+  constexpr uint32_t kMask = 0x00780078u;
+  uint32_t base = 0x41804180u;
+  asm("" : "+v"(base));                              // in a register: and and or in one
+  const uint4 r = make_uint4(((d << 3) & kMask) | base, ((d >> 1) & kMask) | base,
+                             ((d >> 5) & kMask) | base, ((d >> 9) & kMask) | base);
   return __builtin_bit_cast(bf16x8, r);
 }
 
@@ -362,7 +364,7 @@ void int4_tile_kernel(Int4Args a, uint32_t m_tiles, uint32_t runs) {
       if (kSkip && r >= rows_m) continue;
       *reinterpret_cast<u32x4*>(&xs[buffer][r * kPitch + c * 8]) = stage[i];
       const float v = sum_lanes<L>(sum8(stage[i]));
-      if (c % L == 0) sums[buffer][c / L][r] = v;
+      if (c % L == 0) sums[buffer][c / L][r] = kZeros ? v : v * -24.0f;
     }
   };
   float stage_s[kStageG];
@@ -387,7 +389,7 @@ void int4_tile_kernel(Int4Args a, uint32_t m_tiles, uint32_t runs) {
       const int e = i * kThreads + threadIdx.x, r = e / kTileGroups, c = e % kTileGroups;
       Group& to = gs[buffer][r * (kTileGroups + 1) + c];
       if constexpr (kZeros)
-        to = make_float2(stage_s[i], 16.0f + (float)stage_z[i]);
+        to = make_float2(stage_s[i], -16.0f - (float)stage_z[i]);
       else
         to = stage_s[i];
     }
@@ -444,9 +446,9 @@ void int4_tile_kernel(Int4Args a, uint32_t m_tiles, uint32_t runs) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               if constexpr (kZeros)
-                p[i][t] = sum * -sz[t].y;
+                p[i][t] = sum * sz[t].y;
               else
-                p[i][t] = sum * -24.0f;
+                p[i][t] = sum;
             }
           }
 #pragma unroll
@@ -490,10 +492,10 @@ void int4_tile_kernel(Int4Args a, uint32_t m_tiles, uint32_t runs) {
     if (at + 4 * WK == kHeld) gbuffer ^= 1;
   }
 
-  if (WK > 1) {
+  if constexpr (WK > 1) {
     // the waves of a tile add up their parts, in order; xs is free behind the barrier
     constexpr int kTile = MT * NT * 256;
-    static_assert(sizeof(xs) >= sizeof(float) * WN * WK * kTile, "");
+    static_assert(WK == 1 || sizeof(xs) >= sizeof(float) * WN * WK * kTile, "");
     float* part = reinterpret_cast<float*>(xs);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
