@@ -553,33 +553,50 @@ struct Plan {
   uint32_t m, n, waves, runs;
 };
 
+// All times in us, groups of 128, K 4096 unless another is given.
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int64_t blocks = K / 128, units = (blocks + 3) / 4, tiles16 = (N + 15) / 16;
+  auto tiles_of = [&](int64_t m, int64_t n) { return ((M + m - 1) / m) * ((N + n - 1) / n); };
+  // A card's worth of workgroups where the tiles are fewer, as the waves of one leave
+  // a compute unit half idle, in runs of 8 blocks at least, of 4 while units are idle.
   auto runs_of = [&](int64_t m, int64_t n, int64_t want) {
-    const int64_t tiles = ((M + m - 1) / m) * ((N + n - 1) / n);
+    const int64_t tiles = tiles_of(m, n);
     int64_t runs = tiles < want ? want / tiles : 1, most = blocks / 8;
-    // of 8 blocks at least, of 4 while compute units are idle
     if (tiles * most < 256) most = blocks / 4 < 256 / tiles ? blocks / 4 : 256 / tiles;
     runs = runs < most ? runs : most;
     return (uint32_t)(runs < 1 ? 1 : runs);
   };
-  if (M <= 4 && tiles16 <= 2048) {
-    // waves until all workgroups are resident at once, 16 of them to a compute unit
-    int64_t waves = 16;
-    while (waves > 2 && 256 * (16 / waves) < tiles16) waves /= 2;
-    if (waves > units) waves = units;
-    const int64_t per = (units + waves - 1) / waves;
-    return {0, 16, (uint32_t)((units + per - 1) / per), 1};
+  // Up to 4 rows: int4_few_kernel, until its reads of x, one for every 16 rows of the
+  // weight, outweigh it: M 4, N 24576 13.1 against 15.0 of the 16 x 64 tiles, N 28672
+  // 14.8 / 15.3, N 40000 25.0 / 22.0 (M 1: 21.2 / 21.0).
+  if (M <= 4 && tiles16 <= 1792) {
+    // Four waves share K while the card holds them all at once, else two, then one:
+    // N 4096 4.5 with 4, 5.8 with 2, 5.2 with 8; N 11008 8.6 with 4, 8.1 with 2, 9.1
+    // with 1; N 24576 14.6 with 4, 13.9 with 2, 12.2 with 1.  Eight for few tiles
+    // and a long K (N 1024, K 14336: 7.7, 8.5 with 4), each of two units at least
+    // (N 1024, K 4096: 4.1 with 4, 4.4 with 8).
+    int64_t waves = tiles16 <= 64 ? 8 : tiles16 <= 512 ? 4 : tiles16 < 1024 ? 2 : 1;
+    while (waves > 1 && units < 2 * waves) waves /= 2;
+    return {0, 16, (uint32_t)waves, 1};
   }
   if (M <= 16) {
-    if (N >= 64 * 1024) return {16, 128, 8, 1};
-    if (N >= 8 * 1024) return {16, 64, 8, 1};
-    // x read for every 32 or 16 rows of the weight: while that is little
-    const uint32_t n = N >= 6 * 1024 ? 32 : 16;
-    if (M * K * 2 * ((N + n - 1) / n) <= 40 << 20) return {16, n, 8, 1};
-    return {16, 128, 8, runs_of(16, 128, 256)};
+    // A workgroup for each compute unit where N allows it, and no smaller tile, as x is
+    // read for each: M 16, N 4096 8.6 with 16 rows of the weight, 8.8 with 32, 10.4
+    // with 64; N 5120 14.8, 8.9, 10.6; N 8192 15.8, 9.6, 10.7; N 11008 21.9, 13.3, 10.9.
+    // 128 rows where x is heavy, too: N 128000, M 16 68.9 with 64, 64.4 with 128; M 5
+    // 56.9 and 59.3.
+    if (N > 8 * 1024) return {16, M > 8 && N >= 64 * 1024 ? 128u : 64u, 8, 1};
+    // a long K is cut instead: N 4096, K 8192, M 5 / 16 11.1 / 11.9 in four runs of 64
+    // rows, 11.2 / 14.5 whole in 16; K 14336 14.0 / 15.1 and 16.8 / 23.3
+    if (K >= 8 * 1024) return {16, 64, 8, runs_of(16, 64, 256)};
+    return {16, N > 4 * 1024 ? 32u : 16u, 8, 1};
   }
-  if (M <= 32) return {32, 128, 8, runs_of(32, 128, 256)};
+  // 32 rows of x while that is a workgroup for each compute unit at most, beyond it 64,
+  // for which the codes are unpacked half as often: M 64, N 11008 18.5 with 32, 22.5
+  // with 64; M 200, N 4096 18.6 / 23.4; M 100, N 11008 34.4 / 31.6; M 500, N 11008
+  // 98.5 / 63.4.  The runs: M 64, N 4096 17.8 in one, 13.5 in four, 18.2 in eight; of
+  // 64 rows M 300, N 4096 33.0 in one, 27.9 in three.
+  if (M <= 32 || tiles_of(32, 128) <= 256) return {32, 128, 8, runs_of(32, 128, 256)};
   return {64, 128, 4, runs_of(64, 128, 512)};
 }
 

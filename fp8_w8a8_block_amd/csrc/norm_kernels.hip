@@ -197,6 +197,13 @@ void launch_wc(const NormQuantArgs& a, int mode, hipStream_t st) {
 
 }  // namespace
 
+// By the width alone, so that a row's results do not depend on how many come with it.
+// Times in us of 4 / 8191 rows with a residual and codes by groups: H 512 2.5 / 9.8
+// with one wave, 2.6 / 14.4 with four; H 2048 2.7 / 25.1 with four of one chunk, 4.1 /
+// 27.0 with one of four; H 4096 3.1 / 44.4 with eight of one, 3.4 / 44.5 with four of
+// two, 6.1 / 48.2 with one of eight; H 7168 3.8 / 73.1 with eight of two, 4.4 / 75.6
+// with four of four; H 16384 4.9 / 166.5 with sixteen of two, 6.8 / 164.7 with four
+// of eight; H 32768 8.1 / 359 with sixteen of four, 8.4 / 357 with eight of eight.
 hipError_t launch_norm_quant(const NormQuantArgs& a, int mode, hipStream_t st) {
   const int chunks = a.H / 8;
   if (chunks <= 64)
@@ -204,11 +211,11 @@ hipError_t launch_norm_quant(const NormQuantArgs& a, int mode, hipStream_t st) {
   else if (chunks <= 256)
     launch_wc<4, 1>(a, mode, st);
   else if (chunks <= 512)
-    launch_wc<4, 2>(a, mode, st);
+    launch_wc<8, 1>(a, mode, st);
   else if (chunks <= 1024)
-    launch_wc<4, 4>(a, mode, st);
+    launch_wc<8, 2>(a, mode, st);
   else if (chunks <= 2048)
-    launch_wc<8, 4>(a, mode, st);
+    launch_wc<16, 2>(a, mode, st);
   else if (chunks <= 4096)
     launch_wc<16, 4>(a, mode, st);
   else

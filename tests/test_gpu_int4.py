@@ -103,6 +103,14 @@ CASES = {
     "runs_of_a_prompt": (100, 301, 4096, 32, True, 0, 0),
     "runs_even_columns": (70, 300, 4096, 128, False, 0, 0),
     "chunks_of_groups": (3, 20001, 40960, 32, True, 0, 0),
+    "a_batch_of_a_head": (13, 66001, 256, 64, True, 0, 0),
+    "large_tiles": (700, 1601, 512, 128, True, 8, 3),
+    "large_tiles_no_zeros": (650, 1700, 384, 128, False, 0, 0),
+    "large_tiles_middle": (1030, 1030, 256, 64, True, 0, 0),
+    "large_tiles_middle_no_zeros": (1030, 1030, 384, 64, False, 0, 0),
+    "large_tiles_small": (520, 2100, 256, 32, True, 0, 0),
+    "large_tiles_small_no_zeros": (520, 2100, 128, 32, False, 0, 0),
+    "large_tiles_in_runs": (600, 1800, 2048, 128, True, 0, 0),
     "wider_batch": (20, 66000, 128, 32, True, 0, 0),
 }
 
@@ -123,11 +131,11 @@ def test_against_oracle(case):
     assert (out[:, N:] == 7.0).all()
 
 
-@pytest.mark.parametrize("M", [1, 13, 40, 150])
+@pytest.mark.parametrize("M", [1, 13, 40, 150, 1000])
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_each_value_finds_its_weight(M, group):
     """One value of x at a time: the codes come out exactly, so no value meets another's weight."""
-    K, N = 256, 80
+    K, N = 256, 80 if M < 1000 else 1100
     rng = np.random.default_rng(M)
     c, s, z = weights(rng, N, K, group, True)
     s[:] = np.float32(0.25)
