@@ -139,7 +139,7 @@ __device__ __forceinline__ void store_bf16(const Int4Args& a, int64_t m, int64_t
   if (m < a.M && n < a.N) a.out[m * a.ld_out + n] = (uint16_t)pack_bf16(v, v);
 }
 
-constexpr int kFewGroups = 32;                // groups of a row that LDS holds, for each wave
+constexpr int kFewGroups = 64;  // groups of a row that LDS holds, for each of up to four waves
 
 // Up to 4 rows of x with 16 rows of the weight.  The 16 rows of the matrix unit's
 // operand are the 4 rows of x times the 4 products j of a block: row 4 m + j holds
@@ -151,7 +151,7 @@ constexpr int kFewGroups = 32;                // groups of a row that LDS holds,
 // The workgroup's waves share K: each takes a run of units of four blocks, the next
 // of which is in flight while it works on one.
 template <int G, bool kZeros>
-__global__ __launch_bounds__(1024) void int4_few_kernel(Int4Args a) {
+__global__ __launch_bounds__(512) void int4_few_kernel(Int4Args a) {
   constexpr int GPB = 128 / G, J = 4 / GPB;         // products of a group
   constexpr int kStage = kFewGroups / 4;            // of which a thread brings every 4 waves-th
   extern __shared__ float2 few_lds[];               // scales and offsets; then the waves' parts
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(1024) void int4_few_kernel(Int4Args a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = (int)blockDim.x >> 6;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int blocks = a.K / 128, units = (blocks + 3) / 4;
-  const int most = kFewGroups * waves / (4 * GPB);  // units of a chunk of K
+  const int most = kFewGroups * (waves < 4 ? waves : 4) / (4 * GPB);  // units of a chunk of K
   // rows behind the last are read as the last and not stored
   const int rows = (int)(a.N - n0 < 16 ? a.N - n0 : 16);
   const int64_t m = (l16 >> 2) < a.M ? l16 >> 2 : a.M - 1;
@@ -630,7 +630,8 @@ void launch_tile(const Int4Args& a, const Plan& p, int group, hipStream_t st) {
 
 void launch_few(const Int4Args& a, const Plan& p, int group, hipStream_t st) {
   const uint32_t groups = (uint32_t)(a.K / group);
-  const uint32_t held = groups < kFewGroups * p.waves ? groups : kFewGroups * p.waves;
+  const uint32_t most = kFewGroups * (p.waves < 4 ? p.waves : 4);
+  const uint32_t held = groups < most ? groups : most;
   uint32_t lds = 16u * (held | 1u) * sizeof(float2);
   if (lds < p.waves * 256u) lds = p.waves * 256u;
   with_groups(a, group, [&](auto g, auto zeros) {

@@ -103,6 +103,8 @@ CASES = {
     "runs_of_a_prompt": (100, 301, 4096, 32, True, 0, 0),
     "runs_even_columns": (70, 300, 4096, 128, False, 0, 0),
     "chunks_of_groups": (3, 20001, 40960, 32, True, 0, 0),
+    "chunks_of_few_columns": (2, 100, 40960, 32, True, 0, 0),
+    "chunks_of_eight_waves": (1, 64, 65536, 64, False, 0, 0),
     "a_batch_of_a_head": (13, 66001, 256, 64, True, 0, 0),
     "large_tiles": (700, 1601, 512, 128, True, 8, 3),
     "large_tiles_no_zeros": (650, 1700, 384, 128, False, 0, 0),
