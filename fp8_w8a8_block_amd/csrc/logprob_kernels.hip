@@ -594,16 +594,20 @@ struct Plan {
   uint32_t parts, share;        // parts of a row, segments of a part
 };
 
-// One workgroup per row where there are rows enough to fill the card (or little to
-// share), and its segment maxima fit LDS.  Fewer rows are cut into parts of two
-// sweeps, or of whole batches of four: about 1024 parts in all.
+// One workgroup per row, whose segment maxima LDS holds, for a row of up to 16 sweeps
+// or a row for each compute unit; else parts of two sweeps, or of whole batches of
+// four, about 1024 in all.  Times in us: V 32000 fp32 (16 sweeps) 8.3 whole and 8.4 in
+// parts of two for 1 row, 8.8 and 10.0 for 61, bf16 (8 sweeps) 7.8 and 8.4, 8.7 and
+// 9.4; V 128000 bf16 (32 sweeps) 18.3 and 10.0 for 1 row, 19.8 and 13.8 for 61, 21.3
+// whole and 17.6 in parts of four for 128, 22.6 and 25.1 for 256, 55.7 and 68.2 for
+// 1023; fp32 29.6 and 33.6 for 256, 67.6 and 64.6 for 600, 95.0 and 103.1 for 1023.
 Plan plan_of(bool f32, int64_t T, int64_t V) {
   // the row may start anywhere in its first segment
   const int64_t per = f32 ? 32 : 64, segments = (V + 2 * per - 2) / per;
   const int64_t sweeps = (segments + kSweep - 1) / kSweep;
   int64_t each = (sweeps * T + 1023) / 1024;
   each = each <= 2 ? 2 : (each + 3) / 4 * 4;
-  if (T >= 1024 || each >= sweeps) each = sweeps;
+  if (T >= 256 || sweeps <= 16 || each >= sweeps) each = sweeps;
   if (each > kMaxSegments / kSweep) each = kMaxSegments / kSweep;
   const int64_t share = each * kSweep;
   return {(uint32_t)((segments + share - 1) / share), (uint32_t)share};

@@ -63,6 +63,13 @@ CASES = {
     "a_workgroup_each_f32": (1030, 3333, 7, False, 0, 0),
     "long_rows_each": (1024, 24000, 1, True, 0, 0),
     "many_segments": (2, 600000, 64, False, 0, 0),
+    "many_segments_of_many_rows": (260, 300001, 3, True, 0, 0),
+    "sixteen_sweeps": (5, 65000, 40, True, 2, 0),
+    "past_sixteen_sweeps": (5, 65601, 40, True, 3, 5),
+    "parts": (37, 70001, 20, False, 0, 2),
+    "parts_of_batches": (130, 120001, 33, False, 0, 0),
+    "parts_of_batches_bf16": (140, 140000, 5, True, 1, 0),
+    "a_workgroup_for_each_unit": (256, 70000, 5, True, 0, 3),
 }
 
 
@@ -80,11 +87,11 @@ def test_against_oracle(case):
     check(x, tokens, k, scale=0.7)
 
 
-@pytest.mark.parametrize("T", [3, 1030])
+@pytest.mark.parametrize("T, V", [(3, 9000), (1030, 9000), (3, 80000)])
 @pytest.mark.parametrize("bf16", [True, False])
-def test_equal_logits(T, bf16):
+def test_equal_logits(T, V, bf16):
     """Rows of one value, of few values, and with the ties at the end: the lowest indexes first."""
-    V, rng = 9000, np.random.default_rng(2)
+    rng = np.random.default_rng(2)
     x = logits(rng, T, V, bf16)
     x[0] = 1.5
     x[1] = torch.from_numpy(rng.integers(0, 3, V).astype(np.float32)).cuda()
@@ -98,11 +105,11 @@ def test_equal_logits(T, bf16):
         check(x, tokens, k)
 
 
-@pytest.mark.parametrize("T", [4, 1030])
+@pytest.mark.parametrize("T, V", [(4, 10007), (1030, 10007), (4, 80007)])
 @pytest.mark.parametrize("bf16", [True, False])
-def test_masks(T, bf16):
+def test_masks(T, V, bf16):
     """Masked rows: a few logits left, fewer than k, one, none; masks of the lowest value."""
-    V, rng = 10007, np.random.default_rng(3)
+    rng = np.random.default_rng(3)
     x = logits(rng, T, V, bf16)
     low = torch.finfo(x.dtype).min
     x[0] = -torch.inf
@@ -124,10 +131,10 @@ def test_mask_of_the_lowest_value_everywhere_at_scale_one():
     check(x, [1, 3], 4)
 
 
-@pytest.mark.parametrize("T", [5, 1030])
-def test_no_distribution(T):
+@pytest.mark.parametrize("T, V", [(5, 9001), (1030, 9001), (5, 80001)])
+def test_no_distribution(T, V):
     """NaN and +inf make their row NaN and -1, wherever they stand, and no other row."""
-    V, rng = 9001, np.random.default_rng(4)
+    rng = np.random.default_rng(4)
     x = logits(rng, T, V, False)
     x[0, 0], x[1, V - 1], x[2, 4500] = torch.nan, torch.nan, torch.inf
     x[3] = torch.nan
@@ -151,7 +158,7 @@ def test_far_logits():
 
 def test_buffers_are_written_whole_and_nothing_else():
     rng = np.random.default_rng(6)
-    T, V, k = 6, 50000, 3
+    T, V, k = 6, 90000, 3
     x = logits(rng, T, V, True)
     n = fp8.logprobs_workspace_bytes(T, V, k)
     assert n > 0

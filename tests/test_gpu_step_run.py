@@ -222,7 +222,7 @@ def test_captured_steps():
 
 def test_two_at_once_on_other_streams():
     def run(streams):
-        layers = [Layer(4), Layer(5, V=20000)]
+        layers = [Layer(4), Layer(5, V=70001)]
         out = []
         for new in STEPS:
             for s, stream in zip(layers, streams):
@@ -248,7 +248,7 @@ def test_graphs_that_share_a_workspace():
     """4-bit products cut into runs and rows' parts of log probabilities, all in one workspace."""
     rng = np.random.default_rng(6)
     jobs = []
-    for M, N, K, V in ((24, 256, 8192, 40000), (100, 301, 4096, 60001)):
+    for M, N, K, V in ((24, 256, 8192, 130000), (100, 301, 4096, 90001)):
         x = bf16(rng.standard_normal((M, K)))
         w = fp8.int4_quant_weight(bf16(rng.standard_normal((N, K))), 64)
         lo = bf16(rng.standard_normal((4, V)))
@@ -418,7 +418,7 @@ def test_int4_of_many_rows():
         tail_products(x[m:m + 4], codes, scales, zeros, out[m:m + 4], rows)
 
 
-@pytest.mark.parametrize("T, V, ld", [(5, 9001, 2 ** 30 + 5), (1100, 4100000, None), (900, 5000000, None)])
+@pytest.mark.parametrize("T, V, ld", [(5, 9001, 2 ** 30 + 5), (1100, 4100000, None), (250, 18000000, None)])
 def test_logprobs_past_32_bits(T, V, ld):
     g = torch.Generator(device="cuda").manual_seed(T)
     if ld is None:
@@ -441,10 +441,10 @@ def test_logprobs_past_32_bits(T, V, ld):
 def test_logprobs_of_rows_in_parts_and_in_one_launch():
     """A row's whole results do not depend on how many rows are with it."""
     g = torch.Generator(device="cuda").manual_seed(3)
-    x = torch.randn((1100, 20000), device="cuda", generator=g, dtype=torch.bfloat16)
-    tokens = torch.randint(0, 20000, (1100,), device="cuda", generator=g)
+    x = torch.randn((1100, 80000), device="cuda", generator=g, dtype=torch.bfloat16)
+    tokens = torch.randint(0, 80000, (1100,), device="cuda", generator=g)
     for k in (0, 1, 20, 33, 64):
-        assert fp8.logprobs_workspace_bytes(1100, 20000, k) != fp8.logprobs_workspace_bytes(7, 20000, k)
+        assert fp8.logprobs_workspace_bytes(1100, 80000, k) == 0 < fp8.logprobs_workspace_bytes(7, 80000, k)
         a = fp8.token_logprobs(x, tokens, k=k)
         b = fp8.token_logprobs(x[:7], tokens[:7], k=k)
         assert torch.equal(a[1][:7], b[1]) and torch.equal(a[5][:7], b[5])
