@@ -5,8 +5,18 @@
 //   out[m, n] = sum_g s[n, g] ( sum_k x[m, k] (16 + c[n, k]) - (16 + z[n, g]) sum_k x[m, k] ).
 // 16 + c is a bf16 number whose lower mantissa bits are the code: a shift and
 // one and-or turn two codes of the packed layout into a pair of the matrix
-// unit's operand.  The group's sum of x is one more column of the product, by a
-// column of ones, and comes out in the lanes and registers that need it.
+// unit's operand.  The products of a group are exact and its sums fp32, so the
+// scale is applied once per group and result, not rounded into the weight.
+//
+// Few rows are bound by the weight's bytes: K / 2 a row and 4 or 5 for each group.
+// 13 rows with 128000 x 4096 (groups of 128, zero points; 287 MB) take 64.9 us, 4.4
+// TB/s of the 4.9 that a copy reaches; one row with 4096 x 4096 (8.9 MB) 4.5 us and
+// with 4096 x 14336 (groups of 64, zero points; 34 MB) 10.4, of which about 3 are the
+// launch and the first loads' way.  Many rows are bound by what a group costs
+// besides its products: 1000 rows with 11008 x 4096 take 109 us on a constant input
+// and 121 on random ones, for which the clock falls from 2.4 to about 2 GHz;
+// the matrix unit is busy for 38% of the cycles, the vector unit for 59% (unpacking,
+// the groups' scaling, x's way to LDS), LDS for 56%.
 #include <type_traits>
 
 #include "device_common.h"
@@ -149,7 +159,10 @@ constexpr int kFewGroups = 64;  // groups of a row that LDS holds, for each of u
 // x are the same product with ones.
 //
 // The workgroup's waves share K: each takes a run of units of four blocks, the next
-// of which is in flight while it works on one.
+// of which is in flight while it works on one.  The matrix unit has time for the
+// 16-fold product of one row (it is idle otherwise), and reading x as its operand
+// spares the lanes' sum at the end.  The groups' scales go through LDS: read where they
+// are used, 16 rows at 4 bytes each, they cost more requests than the codes.
 template <int G, bool kZeros>
 __global__ __launch_bounds__(512) void int4_few_kernel(Int4Args a) {
   constexpr int GPB = 128 / G, J = 4 / GPB;         // products of a group
@@ -188,8 +201,7 @@ __global__ __launch_bounds__(512) void int4_few_kernel(Int4Args a) {
     const int held = (cn * 4 < blocks - c0 * 4 ? cn * 4 : blocks - c0 * 4) * GPB;
     const int pitch = held | 1;
     if (c0) __syncthreads();
-    // the groups of 16 rows, neighbouring threads along a row: read where they are
-    // used, 16 rows at 4 bytes, they cost more requests than the codes
+    // the groups of 16 rows, neighbouring threads along a row
     float gs[kStage];
     uint32_t gz[kStage];
     const int gr = (int)__umulhi(threadIdx.x, 0xffffffffu / (uint32_t)(4 * waves) + 1u);
@@ -295,6 +307,12 @@ __device__ __forceinline__ float sum_lanes(float v) {
 // LDS, KB blocks at a time, with its sums by groups, and so do the scales and
 // offsets, kTileGroups at a time; both twice, the next while the last are in use.
 // The codes come straight to the waves that multiply them, kAhead blocks ahead.
+//
+// 64 rows of x: a wave unpacks 32 rows of the weight for four products each.  Tried
+// for 1000 rows with 11008 x 4096, 109 us: 64 rows of the weight a wave, with half the
+// LDS reads, but two waves a SIMD, 116 (4096 x 8192 x 8192: 564 and 608); the next
+// product's x read ahead 108.7, with zero points 594 for 564, as registers spill; rows
+// of x at other distances in LDS the same.
 template <int MT, int NT, int WN, int WK, int G, bool kZeros>
 __global__ __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_eu(MT >= 4 ? 3 : 4)))
 void int4_tile_kernel(Int4Args a, uint32_t m_tiles, uint32_t runs) {

@@ -9,9 +9,14 @@
 //
 // The alternatives need no second pass over the row.  It is seen as segments of
 // 128 bytes, whose maxima are kept (the softmax needs them anyway).  512 threads
-// hold the maximum of a run of segments each; the k-th largest of these bounds
+// hold the maximum of some segments each; the k-th largest of these bounds
 // the k-th largest logit from below, so only the segments that reach it are read
 // again, and of them only the logits that reach it are ranked.
+//
+// Many rows are bound by HBM: 2047 rows of 128000 bf16 logits (524 MB) take 105 us,
+// 5.0 TB/s.  Few are bound by the way through two launches and, in the second, four
+// dependent reads with barriers between: one row 4.2 + 6.5 us, 61 rows of 100003 fp32
+// logits (24 MB, 5 us at a copy's rate) 8 + 6.2.
 #include <type_traits>
 
 #include "device_common.h"

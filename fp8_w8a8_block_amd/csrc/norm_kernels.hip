@@ -7,6 +7,9 @@
 // (2 more for a bf16 copy).  A row is held in registers as the bf16 values r,
 // so it is read once; W waves share it, each lane C 16-byte chunks of it, and
 // 16 neighbouring lanes hold a 128-group, whose maximum is a DPP reduction.
+// 8191 rows of 4096 with codes by groups (236 MB) take 44 us, 5.4 TB/s, where a copy
+// of 2 GiB moves 4.9; 2049 of 7168 with the bf16 norm and codes by rows (132 MB) 24 to
+// 28 us; 4 rows 3.1 us, the way through two loads, a sum across waves and a store.
 #include "device_common.h"
 #include "fp8w8a8.h"
 #include "step_launch.h"

@@ -14,7 +14,8 @@
 // has the next head's load in flight while it works on one.  8191 tokens of 32
 // + 8 + 8 heads of 128 (189 MB) take 42 us, 4.5 TB/s, where a large copy moves
 // 4.85; more loads in flight per lane (2, 4, 8 heads) cost occupancy and time
-// (44, 47, 65 us).
+// (44, 47, 65 us).  With positions on three axes they take 44.7 us where the one-axis
+// call takes 40.3: two more positions and four more reads of angles per lane group.
 #include "attention_launch.h"
 #include "device_common.h"
 #include "launch.h"
@@ -27,8 +28,10 @@ namespace {
 // j takes heads j, j + chunks, ..., so that a wave's groups read neighbouring
 // heads and are mostly all at queries, at keys or at values.
 // kAxes: positions on several axes.  Lane c reads the angles of pairs 4 c .. 4 c + 3
-// at the positions of all axes that differ, 16 bytes each, keeps each pair's axis',
-// and hands them to the lanes that turn these pairs.
+// at every axis' position, 16 bytes each, keeps each pair's axis', and hands them to
+// the lanes that turn these pairs.  All reads are on their way together: with a
+// branch for each axis 8191 tokens of 48 heads of 128 took 57 us, without 48 (and 45
+// with twelve heads per group).
 template <int L, bool kInterleaved, bool kAxes>
 __global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, uint32_t chunks) {
   const uint32_t item = blockIdx.x * (256u / L) + threadIdx.x / L;

@@ -41,7 +41,8 @@ extern "C" {
  *            FP8_SCALE_TENSOR: not used
  *   scale    FP8_SCALE_TENSOR: one calibrated fp32 in device memory         (input);
  *            the other modes: not used
- *   r = bf16_RNE(x + residual) (x itself without a residual), residual_out = r
+ *   r = bf16_RNE(x + residual), the sum in fp32 (x itself without a residual),
+ *   residual_out = r
  *   v = r / sqrt(mean(r^2) + eps) * weight                        (in fp32)
  *   y = bf16_RNE(v)
  *   q = E4M3_RNE_saturating(v / s), with s = amax / 448 over each 128 values
@@ -157,7 +158,8 @@ enum { FP8_LOGITS_BF16 = 0, FP8_LOGITS_F32 = 1 };
 /* Largest k of fp8_token_logprobs. */
 #define FP8_MAX_TOP 64
 
-/* Bytes of workspace that fp8_token_logprobs needs on the current device. */
+/* Bytes of workspace that fp8_token_logprobs needs (0 where a row's one workgroup
+ * does all of it). */
 size_t fp8_logprobs_workspace_bytes(int logits_type, int64_t T, int64_t V, int64_t k);
 
 /* fp8_token_logprobs -- what an answer's tokens were worth to the model.
