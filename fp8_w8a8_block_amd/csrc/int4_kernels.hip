@@ -10,8 +10,8 @@
 //
 // Few rows are bound by the weight's bytes: K / 2 a row and 4 or 5 for each group.
 // 13 rows with 128000 x 4096 (groups of 128, zero points; 287 MB) take 64.9 us, 4.4
-// TB/s of the 4.9 that a copy reaches; one row with 4096 x 4096 (8.9 MB) 4.5 us and
-// with 4096 x 14336 (groups of 64, zero points; 34 MB) 10.4, of which about 3 are the
+// TB/s of the 4.9 that a copy reaches; one row with 4096 x 4096 (8.9 MB) 4.2 us and
+// with 4096 x 14336 (groups of 64, zero points; 34 MB) 9.9, of which about 3 are the
 // launch and the first loads' way.  Many rows are bound by what a group costs
 // besides its products: 1000 rows with 11008 x 4096 take 109 us on a constant input
 // and 121 on random ones, for which the clock falls from 2.4 to about 2 GHz;
@@ -312,7 +312,8 @@ __device__ __forceinline__ float sum_lanes(float v) {
 // for 1000 rows with 11008 x 4096, 109 us: 64 rows of the weight a wave, with half the
 // LDS reads, but two waves a SIMD, 116 (4096 x 8192 x 8192: 564 and 608); the next
 // product's x read ahead 108.7, with zero points 594 for 564, as registers spill; rows
-// of x at other distances in LDS the same.
+// of x at other distances in LDS the same; an XCD's workgroups on neighbouring rows of
+// the weight, which then fewer of the L2s read, 125 for 124 (random inputs; 721 for 684).
 template <int MT, int NT, int WN, int WK, int G, bool kZeros>
 __global__ __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_eu(MT >= 4 ? 3 : 4)))
 void int4_tile_kernel(Int4Args a, uint32_t m_tiles, uint32_t runs) {
