@@ -169,8 +169,9 @@ def add_rms_norm_quant(x, weight, residual=None, eps=1e-6, scale_mode="block", s
 
 def add_rms_norm(x, weight, residual=None, eps=1e-6, out=None, residual_out=None):
     """add_rms_norm_quant without the quantization -> the norm, bf16 [T, H]."""
+    dev = _device_of(x, "x")
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
     _norm(x, weight, residual, eps, None, None, out, None, None, residual_out)
     return out
 
@@ -186,14 +187,14 @@ def qk_norm_mrope_cache(query, key, value, q_weight, k_weight, cos_sin, position
     and so on; with in_turn, pair i belongs to axis i % A while that axis has
     pairs left, else to the first.  Tokens with a position outside the table
     on any axis are padding."""
-    dev = _device_of(query, "query")
+    dev, sections = _device_of(query, "query"), tuple(sections)
     stream = _stream_here(dev)
     if stream is not None:
         if query_out is None:
             query_out = torch.empty(query.shape, dtype=torch.bfloat16, device=dev)
         st = _attention._tensor_args.qk_norm_mrope_cache(
             _address("fp8_qk_norm_mrope_cache"), query, key, value, q_weight, k_weight, eps, cos_sin,
-            bool(interleaved), positions, tuple(sections), bool(in_turn), slot_mapping, query_out,
+            bool(interleaved), positions, sections, bool(in_turn), slot_mapping, query_out,
             key_cache, value_cache, k_scale, v_scale, dev, stream)
         if st is not None:
             if st:

@@ -35,6 +35,10 @@ def check(x, tokens, k, scale=1.0, **buffers):
     assert np.array_equal(got["ids"], want["ids"])
     for n in ("logprobs", "entropy", "lse", "top"):
         g, w = got[n].astype(np.float64), want[n]
+        # fp32 holds nothing beyond 2^128 - 2^104: from half a step above it on, 2^103, a
+        # value's nearest is infinity (two logits can be 2^129 apart)
+        with np.errstate(invalid="ignore"):
+            w = np.where(np.abs(w) >= 2.0 ** 128 - 2.0 ** 103, np.sign(w) * np.inf, w)
         assert np.array_equal(np.isnan(g), np.isnan(w)) and np.array_equal(np.isneginf(g), np.isneginf(w)), n
         ok = np.isfinite(w)
         off = np.where(ok, np.abs(np.where(ok, g, 0) - np.where(ok, w, 0)) - tol(w), 0)
@@ -143,6 +147,22 @@ def test_no_distribution(T, V):
     x[0, 1] = 1e30                                              # the NaN's thread is far below
     got = check(x, rng.integers(0, V, T), 6)
     assert (got["ids"][:5] == -1).all() and (got["ids"][5:] >= 0).all()
+
+
+@pytest.mark.parametrize("T, V", [(4, 5000), (300, 5000), (4, 80000)])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_the_types_ends(T, V, bf16):
+    """Differences beyond the type's largest value: weights of 0, and no NaN."""
+    x = logits(np.random.default_rng(8), T, V, bf16)
+    low = torch.finfo(x.dtype).min
+    x[0] = low
+    x[0, 77] = -low
+    x[1, ::3], x[1, 5], x[1, V - 1] = low, -low, -low
+    x[2, :V // 2], x[2, V // 2:] = -torch.inf, low
+    x[3] = -low
+    tokens = np.zeros(T, dtype=np.int64)
+    tokens[:4] = [77, 5, V - 1, 9]
+    check(x, tokens, 9)
 
 
 def test_far_logits():
