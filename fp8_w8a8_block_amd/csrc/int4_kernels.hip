@@ -312,7 +312,9 @@ __device__ __forceinline__ float sum_lanes(float v) {
 // for 1000 rows with 11008 x 4096, 109 us: 64 rows of the weight a wave, with half the
 // LDS reads, but two waves a SIMD, 116 (4096 x 8192 x 8192: 564 and 608); the next
 // product's x read ahead 108.7, with zero points 594 for 564, as registers spill; rows
-// of x at other distances in LDS the same; an XCD's workgroups on neighbouring rows of
+// of x at other distances in LDS the same; products of 32 x 32 x 16, half as many
+// and with no copies of the sums, the same, too (with zero points 4% less); x's way
+// to LDS spread between the products 111; an XCD's workgroups on neighbouring rows of
 // the weight, which then fewer of the L2s read, 125 for 124 (random inputs; 721 for 684).
 template <int MT, int NT, int WN, int WK, int G, bool kZeros>
 __global__ __launch_bounds__(64 * WN * WK) __attribute__((amdgpu_waves_per_eu(MT >= 4 ? 3 : 4)))
