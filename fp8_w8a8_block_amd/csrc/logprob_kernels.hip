@@ -15,8 +15,8 @@
 //
 // Many rows are bound by HBM: 2047 rows of 128000 bf16 logits (524 MB) take 105 us,
 // 5.0 TB/s.  Few are bound by the way through two launches and, in the second, four
-// dependent reads with barriers between: one row 4.2 + 6.5 us, 61 rows of 100003 fp32
-// logits (24 MB, 5 us at a copy's rate) 8 + 6.2.
+// dependent reads with barriers between: one row 4.2 + 5.6 us, 61 rows of 100003 fp32
+// logits (24 MB, 5 us at a copy's rate) 9 + 5.
 #include <type_traits>
 
 #include "device_common.h"
@@ -314,7 +314,7 @@ __device__ __forceinline__ uint32_t kth_key(const float (&v)[N], uint32_t k) {
 }
 
 // f(segment, its maximum) for every segment of a row, eight reads a thread on their way
-// together: one after the other they cost the second launch 1.5 of its 6.5 us.
+// together: one after the other they cost the second launch 1.8 of 6.9 us (3126 segments).
 template <typename F>
 __device__ __forceinline__ void each_segment(const float* maxima, uint32_t segments, F f) {
   constexpr uint32_t U = 8;
@@ -601,13 +601,18 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, u
   const Row<kF32> row(a.logits, a.ld, t, a.V);
   const float c = a.scale * kLog2e;
   const Stats* stats = reinterpret_cast<const Stats*>(a.ws) + (uint64_t)t * parts;
+  // on their way while the bound is found: the token and the first of the parts' sums
+  const int64_t token = a.tokens[t];
+  const uint32_t lane = threadIdx.x & 63u;
+  const Stats near = stats[lane < parts ? lane : 0u];
   const float* maxima = reinterpret_cast<const float*>(reinterpret_cast<const Stats*>(a.ws) +
                                                        (uint64_t)a.T * parts) +
                         (uint64_t)t * parts * share;
   finish(a, t, row, maxima, segments_of(row.lead, a.V, 8 * Row<kF32>::V), sh, [&] {
-    const float mine = token_logit(a, t, row);
+    const float mine = token >= 0 && token < a.V ? row.at((uint32_t)token) : kInf;
     Stats all = {-kInf, 0.0f, 0.0f, 0u};
-    for (uint32_t p = threadIdx.x & 63u; p < parts; p += 64u) {
+    if (lane < parts) all = near;
+    for (uint32_t p = lane + 64u; p < parts; p += 64u) {
       join(all, stats[p].m, stats[p].s, stats[p].d, c);
       all.above += stats[p].above;
     }
