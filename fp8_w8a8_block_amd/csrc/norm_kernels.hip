@@ -46,7 +46,9 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   return t;
 }
 
-// E4M3 codes of 8 fp32 values of a group (|z| <= its amax), as quant8
+// E4M3 codes of 8 fp32 values of a group (|z| <= its amax), as quant8.  amax is fp32
+// here, not bf16: from about 2^-136 down amax / 448 is rounded to few quanta of 2^-149,
+// and the quotient can reach 671.  The conversion does not saturate, so it is cut.
 __device__ __forceinline__ uint2 quant8_group(const float z[8], const GroupDivisor& d) {
   uint32_t o[2];
 #pragma unroll
@@ -54,7 +56,8 @@ __device__ __forceinline__ uint2 quant8_group(const float z[8], const GroupDivis
     float q[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      q[e] = __builtin_copysignf(quotient_abs(z[4 * h + e], d), z[4 * h + e]);
+      q[e] = __builtin_copysignf(__builtin_fminf(quotient_abs(z[4 * h + e], d), kE4M3Max),
+                                 z[4 * h + e]);
     o[h] = e4m3_pack4_mag(q[0], q[1], q[2], q[3]);
   }
   return make_uint2(o[0], o[1]);

@@ -166,6 +166,33 @@ def test_far_values():
                 assert (out[5] == 0).all() and (s[5] == 0).all() and ((q[5] & 0x7f) == 0).all()
 
 
+def test_groups_below_the_scales_resolution():
+    """Maxima of 2^-149 .. 2^-124: amax / 448 has few bits or none, quotients pass 448 and saturate.
+
+    The product of r and the reciprocal root is rounded to 2^-149 there, 2^-150 off at
+    most, that with the weight 1 is exact; the scale is 2^-150 off at most.  2^-149
+    bounds each with the float64 value's own tolerance."""
+    rng = np.random.default_rng(9)
+    T, H, quantum = 20, 384, 2.0 ** -149
+    x = rng.standard_normal((T, H)) * 2.0 ** np.arange(-3, 17)[:, None]     # rms of 2^-3 .. 2^16
+    x[:, 128:256] = rng.integers(-127, 128, (T, 128)) * 2.0 ** -133         # bf16 subnormals
+    x = synth.f32_to_bf16_bits(x.astype(np.float32))
+    for mode, ordinary in (("block", 1.0), ("row", 0.0)):
+        w = np.full(H, ordinary, np.float32)
+        w[128:256] = 1.0
+        w = synth.f32_to_bf16_bits(w)
+        q, s = fp8.add_rms_norm_quant(dev(x), dev(w), eps=1e-6, scale_mode=mode)
+        v, tol = step.norm_ref(x, w, 1e-6)
+        v, tol, q = v[:, 128:256], tol[:, 128:256] + quantum, q[:, 128:256]
+        s = (s[:, 1] if mode == "block" else s).cpu().numpy().astype(np.float64)[:, None]
+        g = np.abs(v).max(-1, keepdims=True) / 448
+        assert (np.abs(s - g) <= quantum + g * 2.0 ** -16).all()
+        assert (s == 0).any() and (g > 1.05 * s).any()        # the sizes meant: none, rounded far down
+        assert ((q & 0x7f) != 0x7f).all()
+        check_quotients(q, np.divide(v, s, out=v * 0, where=s > 0),
+                        np.divide(tol, s, out=tol * 0, where=s > 0))
+
+
 def test_nan_and_infinity_stay_in_their_rows():
     rng = np.random.default_rng(8)
     T, H = 8, 1024
