@@ -50,10 +50,10 @@ extern "C" {
  * What fp8_block_gemm takes: codes and scales as fp8_quant_act and
  * fp8_quant_act_static lay them out, quantized from the fp32 values (not from
  * y).  A group whose s is 0 (zeros, or an amax below 2^-141, whose 448th part
- * fp32 does not hold) gets codes +-0.  The mean of squares neither overflows nor
- * vanishes for any finite r.  A NaN in r makes its row NaN, an infinity gives
- * NaN in its place and zeros elsewhere; the codes of a group whose scale is NaN
- * are unspecified.
+ * fp32 does not hold) gets codes +-0.  Neither the mean of squares nor its root's
+ * reciprocal leaves its range for any finite r; a row of zeros with eps = 0 is NaN
+ * (0 / 0).  A NaN in r makes its row NaN, an infinity gives NaN in its place and
+ * zeros elsewhere; the codes of a group whose scale is NaN are unspecified.
  * At least one of y and q is given.  H a multiple of 128 up to 65536;
  * eps >= 0; base pointers of x, residual, residual_out, weight, y and q
  * 16-byte aligned, ld of bf16 tensors multiples of 8, ld_q of 16.  scale_mode is

@@ -193,6 +193,25 @@ def test_groups_below_the_scales_resolution():
                         np.divide(tol, s, out=tol * 0, where=s > 0))
 
 
+@pytest.mark.parametrize("mode", ["block", "row"])
+def test_roots_beyond_the_types_range(mode):
+    """Rows whose 1 / rms fp32 does not hold, without eps: one far value, subnormals only."""
+    rng = np.random.default_rng(10)
+    for H, values in ((65536, [2.0 ** -122]), (65536, [2.0 ** -133]), (65408, [3 * 2.0 ** -133]),
+                      (1024, [-2.0 ** -133, 2.0 ** -126]), (128, [5 * 2.0 ** -133] * 128),
+                      (256, rng.integers(-127, 128, 256) * 2.0 ** -133),
+                      (4096, rng.standard_normal(4096) * 2.0 ** -127)):
+        x = np.zeros((2, H), np.float32)
+        x[0, rng.permutation(H)[:len(values)]] = values
+        x[1] = -x[0]
+        x, w = synth.f32_to_bf16_bits(x), normal(rng, H)
+        for residual in (None, dev(x * 0)):
+            out = torch.empty((2, H), dtype=torch.bfloat16, device="cuda")
+            q, s = fp8.add_rms_norm_quant(dev(x), dev(w), residual=residual, eps=0.0, scale_mode=mode,
+                                          out=out)
+            check(x, w, 0.0, mode, out, q, s)
+
+
 def test_nan_and_infinity_stay_in_their_rows():
     rng = np.random.default_rng(8)
     T, H = 8, 1024
