@@ -48,14 +48,14 @@ __device__ __forceinline__ float anchor(float m) { return m == -kInf ? 0.0f : m;
 
 // (s, d) relative to the maximum m, moved to the maximum to >= m.  A NaN in s or d
 // stays one, so nothing here may be 0 times infinity, nor drop a factor of 0.
-__device__ __forceinline__ void rebase(float m, float to, float c, float& s, float& d) {
-  const float by = m == -kInf ? 0.0f : __builtin_fmaxf((m - to) * c, -1000.0f);
+__device__ __forceinline__ void rebase(float m, float to, LogprobScale c, float& s, float& d) {
+  const float by = m == -kInf ? 0.0f : __builtin_fmaxf((m - to) * c.c * c.more, -1000.0f);
   const float f = __builtin_amdgcn_exp2f(by);
   d = f * __builtin_fmaf(s, by, d);
   s = f * s;
 }
 
-__device__ __forceinline__ void join(Stats& a, float m, float s, float d, float c) {
+__device__ __forceinline__ void join(Stats& a, float m, float s, float d, LogprobScale c) {
   const float to = __builtin_fmaxf(a.m, m);
   rebase(a.m, to, c, a.s, a.d);
   rebase(m, to, c, s, d);
@@ -85,7 +85,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // the wave's sums, in every lane (above is not touched)
-__device__ __forceinline__ void join_wave(Stats& a, float c) {
+__device__ __forceinline__ void join_wave(Stats& a, LogprobScale c) {
   const float m = wave_fold(a.m, [](float x, float y) { return __builtin_fmaxf(x, y); });
   rebase(a.m, m, c, a.s, a.d);
   a.m = m;
@@ -155,7 +155,7 @@ __device__ __forceinline__ float segment_max(float v) {
 // One batch of U vectors a thread, kThreads apart: x is theirs.  `segments` of the
 // batch are the part's.
 template <bool kF32, int U>
-__device__ __forceinline__ void take(const float (&x)[U][Row<kF32>::V], float c, float mine,
+__device__ __forceinline__ void take(const float (&x)[U][Row<kF32>::V], LogprobScale c, float mine,
                                      Stats& a, float* maxima, uint32_t segments) {
   constexpr int V = Row<kF32>::V;
   float top[U], m = a.m;
@@ -168,12 +168,21 @@ __device__ __forceinline__ void take(const float (&x)[U][Row<kF32>::V], float c,
   }
   rebase(a.m, m, c, a.s, a.d);
   a.m = m;
+  // One product a value less: (x more - from more) c.  Where from 2 may be beyond fp32,
+  // too, a difference is 0 or 2^-24 and more, of weight 0 with any c of that size.
   const float from = anchor(m);
+  float more = 1.0f, by = c.c;
+  if (c.more != 1.0f) {                             // for all threads alike
+    const bool far = __builtin_fabsf(from) >= 1.0f;
+    more = far ? 1.0f : c.more;
+    by = far ? 0x1.fffffep+127f : c.c;
+  }
+  const float lift = -from * more;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float t = (x[u][e] - from) * c, w = __builtin_amdgcn_exp2f(t);
+      const float t = __builtin_fmaf(x[u][e], more, lift) * by, w = __builtin_amdgcn_exp2f(t);
       a.s += w;
       // a weight of 0 has an exponent of -inf, and no part in D
       a.d = __builtin_fmaf(w, __builtin_fmaxf(t, -1000.0f), a.d);
@@ -202,7 +211,7 @@ __device__ __forceinline__ void load_batch(const Row<kF32>& row, uint32_t seg, u
 }
 template <bool kF32, int U>
 __device__ __forceinline__ void take_edge(const Row<kF32>& row, const uint4 (&r)[U], uint32_t seg,
-                                          uint32_t last, float c, float mine, Stats& a,
+                                          uint32_t last, LogprobScale c, float mine, Stats& a,
                                           float* maxima) {
   constexpr int V = Row<kF32>::V;
   const uint32_t lo = (row.lead + V - 1) / V, hi = (row.lead + row.n) / V, end = last * 8u;
@@ -227,7 +236,7 @@ __device__ __forceinline__ void take_edge(const Row<kF32>& row, const uint4 (&r)
 // the whole workgroup in every thread.  get_mine reads the token's logit, once the
 // first loads of the row are on their way.
 template <bool kF32, typename F>
-__device__ Stats stream(const Row<kF32>& row, uint32_t first, uint32_t last, float c, float& mine,
+__device__ Stats stream(const Row<kF32>& row, uint32_t first, uint32_t last, LogprobScale c, float& mine,
                         float* maxima, F get_mine) {
   constexpr int V = Row<kF32>::V, U = 4;
   __shared__ Stats shared[kThreads / 64];
@@ -559,7 +568,7 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
   __shared__ Select sh;
   const int64_t t = blockIdx.x;
   const Row<kF32> row(a.logits, a.ld, t, a.V);
-  const float c = a.scale * kLog2e;
+  const LogprobScale c = a.unit;
   float mine;
   const uint32_t segments = segments_of(row.lead, a.V, 8 * Row<kF32>::V);
   const Stats all = stream(row, 0u, segments, c, mine, maxima,
@@ -579,7 +588,7 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobArgs a, u
   const int64_t t = blockIdx.x / parts;
   const uint32_t p = blockIdx.x - (uint32_t)t * parts;
   const Row<kF32> row(a.logits, a.ld, t, a.V);
-  const float c = a.scale * kLog2e;
+  const LogprobScale c = a.unit;
   float mine;
   const uint32_t segments = segments_of(row.lead, a.V, 8 * Row<kF32>::V);
   const uint32_t first = p * share < segments ? p * share : segments;
@@ -599,7 +608,7 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, u
   __shared__ Select sh;
   const int64_t t = blockIdx.x;
   const Row<kF32> row(a.logits, a.ld, t, a.V);
-  const float c = a.scale * kLog2e;
+  const LogprobScale c = a.unit;
   const Stats* stats = reinterpret_cast<const Stats*>(a.ws) + (uint64_t)t * parts;
   // on their way while the bound is found: the token and the first of the parts' sums
   const int64_t token = a.tokens[t];
@@ -680,7 +689,9 @@ static hipError_t launch(const LogprobArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_logprobs(const LogprobArgs& a, bool f32, hipStream_t st) {
+hipError_t launch_logprobs(LogprobArgs a, bool f32, hipStream_t st) {
+  const bool half = a.scale >= 0x1p+126f;
+  a.unit = {(half ? a.scale * 0.5f : a.scale) * kLog2e, half ? 2.0f : 1.0f};
   return f32 ? launch<true>(a, st) : launch<false>(a, st);
 }
 

@@ -50,6 +50,11 @@ size_t int4_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int4_linear(const Int4Args& a, int group, hipStream_t st);
 uint64_t int4_linear_items(int64_t M, int64_t N, int64_t K);
 
+// (x - from) scale log2(e) is (x - from) c more; c alone would be beyond fp32 for scales
+// from 2.36e38 on, so `more` is 2 for such and 1 for others
+struct LogprobScale {
+  float c, more;
+};
 struct LogprobArgs {
   const void* logits;
   int64_t ld;
@@ -64,9 +69,10 @@ struct LogprobArgs {
   float* top;
   int32_t* ids;
   uint8_t* ws;
+  LogprobScale unit;            // of `scale`, by the launcher
 };
 size_t logprobs_workspace(bool f32, int64_t T, int64_t V, int64_t k);
-hipError_t launch_logprobs(const LogprobArgs& a, bool f32, hipStream_t st);
+hipError_t launch_logprobs(LogprobArgs a, bool f32, hipStream_t st);
 uint64_t logprobs_items(bool f32, int64_t T, int64_t V, int64_t k);
 
 }  // namespace fp8k

@@ -176,7 +176,8 @@ size_t fp8_logprobs_workspace_bytes(int logits_type, int64_t T, int64_t V, int64
  *            both NULL if k is 0                                          (output)
  * One pass over the logits, sums in fp32.  A logit of -inf has probability 0: its log
  * probability is -inf, and it comes among the alternatives after all others.  A log
- * probability below fp32's range is -inf, too.
+ * probability below fp32's range is -inf, too, and an lse beyond it an infinity,
+ * beside log probabilities as they are.
  * A row of -inf only has lse and log probabilities -inf and entropy 0.  A row
  * with a NaN or +inf is no distribution: its log probabilities, entropy and
  * lse are NaN, its ranks and ids -1.  A token outside [0, V) is padding: log

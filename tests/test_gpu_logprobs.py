@@ -176,6 +176,30 @@ def test_far_logits():
         check(x, [7, 8, 9], 10, scale=scale)
 
 
+FAR_SCALES = (float(torch.finfo(torch.float32).max), 2.5e38, 2.0 ** 126)
+
+
+@pytest.mark.parametrize("T, V", [(5, 7001), (300, 7001), (5, 90001)])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_largest_scales(T, V, bf16):
+    """Scales up to the type's largest (a temperature of 0, cut there): the largest logits
+    share the probability, and logits that small have a distribution of their own."""
+    x = logits(np.random.default_rng(9), T, V, bf16)
+    store = x.clone()
+    tokens = np.zeros(T, dtype=np.int64)
+    for scale in FAR_SCALES:
+        x.copy_(store)
+        x[1, 5], x[1, V - 2] = 40.0, 40.0                      # two equal maxima
+        x[2] = 3.0
+        x[3, 7:] = -torch.inf
+        x[-1] = 0.0
+        tokens[:5] = [int(x[0].float().argmax()), 5, 9, 8, V - 1]
+        got = check(x, tokens, 5, scale=scale)
+        assert (got["logprobs"][0] == 0) == ((x[0] == x[0].max()).sum().item() == 1)
+        x.copy_(store * (1.0 / scale))                         # subnormal values
+        check(x, tokens, 5, scale=scale)
+
+
 def test_buffers_are_written_whole_and_nothing_else():
     rng = np.random.default_rng(6)
     T, V, k = 6, 90000, 3
