@@ -46,16 +46,51 @@ struct Stats {
 
 __device__ __forceinline__ float anchor(float m) { return m == -kInf ? 0.0f : m; }
 
+// (x - from) pre, in fp32's range where the difference is not
+__device__ __forceinline__ float apart(float x, float from, const LogprobScale& u) {
+  return __builtin_fmaf(x, u.pre, -from * u.pre);
+}
+
+// What turns differences of logits into exponents.  kFar: a scale so small that
+// differences beyond fp32 have a weight, or so large that scale log2(e) is beyond it;
+// else c is that, and pre and post are left out (2 % of the time of a few rows).
+template <bool kFar>
+struct Unit {
+  LogprobScale u;
+
+  // (x - from) scale log2(e)
+  __device__ __forceinline__ float exponent(float x, float from) const {
+    return kFar ? apart(x, from, u) * u.c * u.post : (x - from) * u.c;
+  }
+  // The same for many x, a product less with `post`: (x post - from post) c.  Where from 2
+  // may be beyond fp32, too, a difference is 0 or 2^-24 and more, of weight 0 with any c
+  // of that size.
+  struct From {
+    float from, pre, lift, c;
+    __device__ __forceinline__ float exponent(float x) const {
+      return kFar ? __builtin_fmaf(x, pre, lift) * c : (x - from) * c;
+    }
+  };
+  __device__ __forceinline__ From relative_to(float from) const {
+    if (!kFar) return {from, 1.0f, 0.0f, u.c};
+    const bool far = u.post != 1.0f && __builtin_fabsf(from) >= 1.0f;
+    const float pre = far ? 1.0f : u.pre * u.post;
+    return {from, pre, -from * pre, far ? 0x1.fffffep+127f : u.c};
+  }
+};
+
 // (s, d) relative to the maximum m, moved to the maximum to >= m.  A NaN in s or d
 // stays one, so nothing here may be 0 times infinity, nor drop a factor of 0.
-__device__ __forceinline__ void rebase(float m, float to, LogprobScale c, float& s, float& d) {
-  const float by = m == -kInf ? 0.0f : __builtin_fmaxf((m - to) * c.c * c.more, -1000.0f);
+template <bool kFar>
+__device__ __forceinline__ void rebase(float m, float to, Unit<kFar> c, float& s, float& d) {
+  const float by = m == -kInf ? 0.0f : __builtin_fmaxf(c.exponent(m, to), -1000.0f);
   const float f = __builtin_amdgcn_exp2f(by);
   d = f * __builtin_fmaf(s, by, d);
   s = f * s;
 }
 
-__device__ __forceinline__ void join(Stats& a, float m, float s, float d, LogprobScale c) {
+template <bool kFar>
+__device__ __forceinline__ void join(Stats& a, float m, float s, float d, Unit<kFar> c) {
   const float to = __builtin_fmaxf(a.m, m);
   rebase(a.m, to, c, a.s, a.d);
   rebase(m, to, c, s, d);
@@ -85,7 +120,8 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // the wave's sums, in every lane (above is not touched)
-__device__ __forceinline__ void join_wave(Stats& a, LogprobScale c) {
+template <bool kFar>
+__device__ __forceinline__ void join_wave(Stats& a, Unit<kFar> c) {
   const float m = wave_fold(a.m, [](float x, float y) { return __builtin_fmaxf(x, y); });
   rebase(a.m, m, c, a.s, a.d);
   a.m = m;
@@ -154,8 +190,8 @@ __device__ __forceinline__ float segment_max(float v) {
 
 // One batch of U vectors a thread, kThreads apart: x is theirs.  `segments` of the
 // batch are the part's.
-template <bool kF32, int U>
-__device__ __forceinline__ void take(const float (&x)[U][Row<kF32>::V], LogprobScale c, float mine,
+template <bool kF32, int U, bool kFar>
+__device__ __forceinline__ void take(const float (&x)[U][Row<kF32>::V], Unit<kFar> c, float mine,
                                      Stats& a, float* maxima, uint32_t segments) {
   constexpr int V = Row<kF32>::V;
   float top[U], m = a.m;
@@ -168,21 +204,12 @@ __device__ __forceinline__ void take(const float (&x)[U][Row<kF32>::V], LogprobS
   }
   rebase(a.m, m, c, a.s, a.d);
   a.m = m;
-  // One product a value less: (x more - from more) c.  Where from 2 may be beyond fp32,
-  // too, a difference is 0 or 2^-24 and more, of weight 0 with any c of that size.
-  const float from = anchor(m);
-  float more = 1.0f, by = c.c;
-  if (c.more != 1.0f) {                             // for all threads alike
-    const bool far = __builtin_fabsf(from) >= 1.0f;
-    more = far ? 1.0f : c.more;
-    by = far ? 0x1.fffffep+127f : c.c;
-  }
-  const float lift = -from * more;
+  const auto from = c.relative_to(anchor(m));
 #pragma unroll
   for (int u = 0; u < U; ++u) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float t = __builtin_fmaf(x[u][e], more, lift) * by, w = __builtin_amdgcn_exp2f(t);
+      const float t = from.exponent(x[u][e]), w = __builtin_amdgcn_exp2f(t);
       a.s += w;
       // a weight of 0 has an exponent of -inf, and no part in D
       a.d = __builtin_fmaf(w, __builtin_fmaxf(t, -1000.0f), a.d);
@@ -209,9 +236,9 @@ __device__ __forceinline__ void load_batch(const Row<kF32>& row, uint32_t seg, u
     r[u] = lo < hi ? row.base[v] : make_uint4(0u, 0u, 0u, 0u);
   }
 }
-template <bool kF32, int U>
+template <bool kF32, int U, bool kFar>
 __device__ __forceinline__ void take_edge(const Row<kF32>& row, const uint4 (&r)[U], uint32_t seg,
-                                          uint32_t last, LogprobScale c, float mine, Stats& a,
+                                          uint32_t last, Unit<kFar> c, float mine, Stats& a,
                                           float* maxima) {
   constexpr int V = Row<kF32>::V;
   const uint32_t lo = (row.lead + V - 1) / V, hi = (row.lead + row.n) / V, end = last * 8u;
@@ -235,9 +262,9 @@ __device__ __forceinline__ void take_edge(const Row<kF32>& row, const uint4 (&r)
 // Segments first .. last - 1 of a row, their maxima to maxima[0 ..]; the sums of
 // the whole workgroup in every thread.  get_mine reads the token's logit, once the
 // first loads of the row are on their way.
-template <bool kF32, typename F>
-__device__ Stats stream(const Row<kF32>& row, uint32_t first, uint32_t last, LogprobScale c, float& mine,
-                        float* maxima, F get_mine) {
+template <bool kF32, bool kFar, typename F>
+__device__ Stats stream(const Row<kF32>& row, uint32_t first, uint32_t last, Unit<kFar> c,
+                        float& mine, float* maxima, F get_mine) {
   constexpr int V = Row<kF32>::V, U = 4;
   __shared__ Stats shared[kThreads / 64];
   Stats a = {-kInf, 0.0f, 0.0f, 0u};
@@ -530,7 +557,9 @@ __device__ void finish(const LogprobArgs& a, int64_t t, const Row<kF32>& row,
   const float from = anchor(all.m), log_s = __builtin_amdgcn_logf(all.s);
   const float nan = __builtin_nanf("");
   auto log_p = [&](float x) {
-    return !good ? nan : x == -kInf ? -kInf : __builtin_fmaf(x - from, a.scale, -log_s * kLn2);
+    return !good        ? nan
+           : x == -kInf ? -kInf
+                        : __builtin_fmaf(apart(x, from, a.unit), a.unit.z, -log_s * kLn2);
   };
   if (threadIdx.x == 0) {
     const bool given = a.tokens[t] >= 0 && a.tokens[t] < a.V;
@@ -562,13 +591,13 @@ __device__ __forceinline__ uint32_t segments_of(uint32_t lead, int64_t vocab, in
 }
 
 // One workgroup per row: the pass and the selection.
-template <bool kF32>
+template <bool kF32, bool kFar>
 __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
   extern __shared__ float maxima[];
   __shared__ Select sh;
   const int64_t t = blockIdx.x;
   const Row<kF32> row(a.logits, a.ld, t, a.V);
-  const LogprobScale c = a.unit;
+  const Unit<kFar> c = {a.unit};
   float mine;
   const uint32_t segments = segments_of(row.lead, a.V, 8 * Row<kF32>::V);
   const Stats all = stream(row, 0u, segments, c, mine, maxima,
@@ -582,13 +611,13 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
 }
 
 // Few rows: the pass over `parts` parts of each, every one of `share` segments, ...
-template <bool kF32>
+template <bool kF32, bool kFar>
 __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobArgs a, uint32_t parts,
                                                                 uint32_t share) {
   const int64_t t = blockIdx.x / parts;
   const uint32_t p = blockIdx.x - (uint32_t)t * parts;
   const Row<kF32> row(a.logits, a.ld, t, a.V);
-  const LogprobScale c = a.unit;
+  const Unit<kFar> c = {a.unit};
   float mine;
   const uint32_t segments = segments_of(row.lead, a.V, 8 * Row<kF32>::V);
   const uint32_t first = p * share < segments ? p * share : segments;
@@ -602,13 +631,13 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobArgs a, u
 }
 
 // ... and what follows from them.
-template <bool kF32>
+template <bool kF32, bool kFar>
 __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, uint32_t parts,
                                                                 uint32_t share) {
   __shared__ Select sh;
   const int64_t t = blockIdx.x;
   const Row<kF32> row(a.logits, a.ld, t, a.V);
-  const LogprobScale c = a.unit;
+  const Unit<kFar> c = {a.unit};
   const Stats* stats = reinterpret_cast<const Stats*>(a.ws) + (uint64_t)t * parts;
   // on their way while the bound is found: the token and the first of the parts' sums
   const int64_t token = a.tokens[t];
@@ -672,27 +701,32 @@ uint64_t logprobs_items(bool f32, int64_t T, int64_t V, int64_t k) {
   return (uint64_t)T * plan_of(f32, T, V).parts * kThreads;
 }
 
-template <bool kF32>
+template <bool kF32, bool kFar>
 static hipError_t launch(const LogprobArgs& a, hipStream_t st) {
   const Plan p = plan_of(kF32, a.T, a.V);
   if (p.parts == 1) {
-    hipLaunchKernelGGL(logprob_kernel<kF32>, dim3((uint32_t)a.T), dim3(kThreads),
+    hipLaunchKernelGGL((logprob_kernel<kF32, kFar>), dim3((uint32_t)a.T), dim3(kThreads),
                        p.share * sizeof(float), st, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(logprob_part_kernel<kF32>, dim3((uint32_t)(a.T * p.parts)), dim3(kThreads), 0,
-                     st, a, p.parts, p.share);
+  hipLaunchKernelGGL((logprob_part_kernel<kF32, kFar>), dim3((uint32_t)(a.T * p.parts)),
+                     dim3(kThreads), 0, st, a, p.parts, p.share);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(logprob_join_kernel<kF32>, dim3((uint32_t)a.T), dim3(kThreads), 0, st, a,
-                     p.parts, p.share);
+  hipLaunchKernelGGL((logprob_join_kernel<kF32, kFar>), dim3((uint32_t)a.T), dim3(kThreads), 0,
+                     st, a, p.parts, p.share);
   return hipGetLastError();
 }
 
 hipError_t launch_logprobs(LogprobArgs a, bool f32, hipStream_t st) {
-  const bool half = a.scale >= 0x1p+126f;
-  a.unit = {(half ? a.scale * 0.5f : a.scale) * kLog2e, half ? 2.0f : 1.0f};
-  return f32 ? launch<true>(a, st) : launch<false>(a, st);
+  // from 2^-100 on a difference beyond fp32 has a weight of 0, as its infinity does
+  const bool far = a.scale < 0x1p-100f || a.scale >= 0x1p+126f;
+  a.unit.pre = a.scale < 1.0f ? 0.5f : 1.0f;
+  a.unit.post = a.scale >= 0x1p+126f ? 2.0f : 1.0f;
+  a.unit.z = a.scale / a.unit.pre;
+  a.unit.c = (far ? a.unit.z / a.unit.post : a.scale) * kLog2e;
+  if (far) return f32 ? launch<true, true>(a, st) : launch<false, true>(a, st);
+  return f32 ? launch<true, false>(a, st) : launch<false, false>(a, st);
 }
 
 }  // namespace fp8k

@@ -50,10 +50,11 @@ size_t int4_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int4_linear(const Int4Args& a, int group, hipStream_t st);
 uint64_t int4_linear_items(int64_t M, int64_t N, int64_t K);
 
-// (x - from) scale log2(e) is (x - from) c more; c alone would be beyond fp32 for scales
-// from 2.36e38 on, so `more` is 2 for such and 1 for others
+// (x - from) scale is ((x - from) pre) z.  The difference may be beyond fp32 where this is
+// not, for scales below 1: pre is 0.5 for such, else 1.  scale log2(e) is c, in the kernels
+// of far scales c pre post; it is beyond fp32 from 2.36e38 on: post is 2 there, else 1.
 struct LogprobScale {
-  float c, more;
+  float pre, z, c, post;
 };
 struct LogprobArgs {
   const void* logits;

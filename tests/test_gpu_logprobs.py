@@ -200,6 +200,23 @@ def test_largest_scales(T, V, bf16):
         check(x, tokens, 5, scale=scale)
 
 
+@pytest.mark.parametrize("T, V", [(4, 5000), (300, 5000), (4, 80000)])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_smallest_scales(T, V, bf16):
+    """Logits up to the type's ends under scales that bring them back: their differences pass
+    fp32's range, scale times them does not."""
+    x = logits(np.random.default_rng(10), T, V, bf16)
+    low = torch.finfo(x.dtype).min
+    x.copy_((x.float().clamp(-9, 9) * 3.7e37).to(x.dtype))
+    x[0, 3], x[0, 4] = low, -low
+    x[1, ::2], x[1, 1::2] = low, -low
+    x[2, 100:] = -torch.inf
+    tokens = np.arange(T, dtype=np.int64) % V
+    tokens[:3] = [3, 2, 50]
+    for scale in (1e-38, 2e-38, 1e-37, 1e-44, 2.0 ** -100, 7e-31, 1e-20, 0.3):
+        check(x, tokens, 9, scale=scale)
+
+
 def test_buffers_are_written_whole_and_nothing_else():
     rng = np.random.default_rng(6)
     T, V, k = 6, 90000, 3
