@@ -149,6 +149,46 @@ __device__ __forceinline__ void store_bf16(const Int4Args& a, int64_t m, int64_t
   if (m < a.M && n < a.N) a.out[m * a.ld_out + n] = (uint16_t)pack_bf16(v, v);
 }
 
+// Not finite: a sum left fp32's range on the way, or x or the weight's scales hold what is
+// not finite.
+__device__ __forceinline__ bool beyond(float v) { return !(__builtin_fabsf(v) < __builtin_huge_valf()); }
+
+// out[m, n] for a result that is `beyond`, from the definition in 64 bits: x (16 + code) and
+// its sums leave fp32's range from |x| = 2^112 on, where s (c - z) x need not.  All lanes of
+// a wave call, 16 neighbouring ones with one m, whose row of x they search together for an
+// infinity or a NaN, which makes it NaN; only those that want it get a result.
+__device__ float again(const Int4Args& a, int64_t m, int64_t n, int group, bool wanted) {
+  const uint16_t* x = a.x + m * a.ld_x;
+  uint32_t bad = 0u;
+  for (int k = (threadIdx.x & 15u) * 8; k < a.K; k += 128) {
+    const u32x4 r = *reinterpret_cast<const u32x4*>(x + k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bad |= ((r[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+  }
+  if (__ballot(bad != 0u) >> (threadIdx.x & 48u) & 0xffffu) return __builtin_nanf("");
+  if (!wanted) return 0.0f;
+  const uint8_t* w = a.codes + n * (a.K / 2);
+  double sum = 0.0;
+#pragma unroll 1
+  for (int k0 = 0; k0 < a.K; k0 += group) {
+    const int64_t g = n * (a.K / group) + k0 / group;
+    const int z = a.zeros ? a.zeros[g] : 8;
+    double part = 0.0;
+#pragma unroll 1
+    for (int k = k0; k < k0 + group; k += 8) {
+      const u32x4 r = *reinterpret_cast<const u32x4*>(x + k);
+      const uint32_t d = *reinterpret_cast<const uint32_t*>(w + k / 2);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = (e & 1) ? bf16_hi(r[e / 2]) : bf16_lo(r[e / 2]);
+        part += (double)v * (double)((int)(d >> (16 * (e & 1) + 4 * (e / 2)) & 15u) - z);
+      }
+    }
+    sum += (double)a.scales[g] * part;
+  }
+  return (float)sum;
+}
+
 constexpr int kFewGroups = 64;  // groups of a row that LDS holds, for each of up to four waves
 
 // Up to 4 rows of x with 16 rows of the weight.  The 16 rows of the matrix unit's
@@ -271,6 +311,11 @@ __global__ __launch_bounds__(512) void int4_few_kernel(Int4Args a) {
     if (wave != 0) return;
 #pragma unroll 4
     for (int i = 1; i < waves; ++i) acc += part[i * 64 + lane];
+  }
+  const bool redo = beyond(acc) && q < a.M && l16 < rows;
+  if (__ballot(redo)) {                             // the lanes' row of x is the one they read
+    const float v = again(a, q < a.M ? q : a.M - 1, n0 + (l16 < rows ? l16 : 0), G, redo);
+    acc = redo ? v : acc;
   }
   store_bf16(a, q, n0 + l16, acc);
 }
@@ -534,6 +579,7 @@ void int4_tile_kernel(Int4Args a, uint32_t m_tiles, uint32_t runs) {
           acc[i][t] += *reinterpret_cast<const f32x4*>(
               &part[(((wave + o) * MT + i) * NT + t) * 256 + lane * 4]);
   }
+  uint32_t redo = 0u;                               // a bit for each result
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -546,26 +592,51 @@ void int4_tile_kernel(Int4Args a, uint32_t m_tiles, uint32_t runs) {
           store_bf16(a, m, n, acc[i][t][e]);
         else if (m < a.M && n < a.N)
           a.parts[((int64_t)run * a.M + m) * a.N + n] = acc[i][t][e];
+        if (beyond(acc[i][t][e]) && m < a.M && n < a.N) redo |= 1u << ((i * NT + t) * 4 + e);
       }
+  if (runs > 1 || __ballot(redo != 0u) == 0u) return;
+#pragma unroll 1
+  for (int b = 0; b < MT * NT * 4; ++b) {
+    const bool mine = redo >> b & 1u;
+    if (__ballot(mine) == 0u) continue;
+    const int64_t m = m0 + 16 * (b / (NT * 4)) + 4 * q + b % 4;
+    const int64_t n = n0 + 16 * (wn * NT + b / 4 % NT) + l16;
+    const float v = again(a, m < a.M ? m : a.M - 1, n, G, mine);
+    if (mine) store_bf16(a, m, n, v);
+  }
 }
 
 // The runs' sums, added in the order of K: a row of out per blockIdx.y.
-__global__ __launch_bounds__(256) void int4_join_kernel(Int4Args a, uint32_t runs) {
+__global__ __launch_bounds__(256) void int4_join_kernel(Int4Args a, uint32_t runs, int group) {
   const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, m = blockIdx.y;
   const int64_t total = a.M * a.N;
   const float* part = a.parts + m * a.N + n;
+  f32x4 v = {};
   if (n + 4 <= a.N && a.N % 4 == 0) {
-    f32x4 v = *reinterpret_cast<const f32x4*>(part);
+    v = *reinterpret_cast<const f32x4*>(part);
 #pragma unroll 4
     for (uint32_t r = 1; r < runs; ++r) v += *reinterpret_cast<const f32x4*>(part + r * total);
+  } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) store_bf16(a, m, n + e, v[e]);
-    return;
+    for (int e = 0; e < 4; ++e) {
+      if (n + e >= a.N) break;
+      v[e] = part[e];
+      for (uint32_t r = 1; r < runs; ++r) v[e] += part[r * total + e];
+    }
   }
-  for (int e = 0; e < 4 && n + e < a.N; ++e) {
-    float v = part[e];
-    for (uint32_t r = 1; r < runs; ++r) v += part[r * total + e];
-    store_bf16(a, m, n + e, v);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) store_bf16(a, m, n + e, v[e]);
+  uint32_t redo = 0u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (beyond(v[e])) redo |= 1u << e;              // 0 behind the last
+  if (__ballot(redo != 0u) == 0u) return;
+#pragma unroll 1
+  for (int e = 0; e < 4; ++e) {
+    const bool mine = redo >> e & 1u;
+    if (__ballot(mine) == 0u) continue;
+    const float r = again(a, m, n + e, group, mine);
+    if (mine) store_bf16(a, m, n + e, r);
   }
 }
 
@@ -689,7 +760,7 @@ hipError_t launch_int4_linear(const Int4Args& a, int group, hipStream_t st) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.runs == 1) return e;
   hipLaunchKernelGGL(int4_join_kernel, dim3((uint32_t)((a.N + 1023) / 1024), (uint32_t)a.M),
-                     dim3(256), 0, st, a, p.runs);
+                     dim3(256), 0, st, a, p.runs, group);
   return hipGetLastError();
 }
 

@@ -137,7 +137,9 @@ size_t fp8_int4_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * The matrix unit multiplies bf16 x with the exact integers 16 + code; the sums
  * of a group are fp32, 16 + zero times the group's sum of x is taken off in
  * fp32, and the scaled groups are summed in fp32.  Nothing is rounded below
- * that but the result.  A row of x that holds an infinity or a NaN gives NaN.
+ * that but the result.  Where a sum leaves fp32's range on the way (|x| from
+ * about 2^112 on), the result is formed again in 64 bits, by a few lanes: right, but
+ * slow.  A row of x that holds an infinity or a NaN gives NaN.
  * group 32, 64 or 128; K a positive multiple of 128 below 2^24; any N >= 1 and
  * M >= 0 (M = 0 does nothing); x, codes and scales 16-byte aligned, out 2-byte aligned,
  * ld_x a multiple of 8, ld_out any >= N.  Zeros above 15 are taken as they are.

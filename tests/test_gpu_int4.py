@@ -152,6 +152,40 @@ def test_each_value_finds_its_weight(M, group):
             break
 
 
+# M, N, K: few rows, each tile, runs of K
+FAR = [(1, 80, 512), (4, 37, 384), (13, 80, 512), (9, 5000, 256), (6, 9000, 256), (9, 66000, 128),
+       (24, 515, 8192), (40, 130, 256), (100, 301, 4096), (700, 1601, 256)]
+
+
+@pytest.mark.parametrize("M, N, K", FAR)
+@pytest.mark.parametrize("group, zeros", [(32, True), (64, False), (128, True), (128, False)])
+def test_values_near_the_types_end(M, N, K, group, zeros):
+    """x (16 + code) or its sums leave fp32's range where the result does not: right all the same."""
+    rng = np.random.default_rng([M, N, group])
+    x = rng.standard_normal((M, K)).astype(np.float32)
+    x[::3] = np.clip(x[::3], -1.9, 1.9) * np.float32(2.0 ** 127)
+    x[1::3, ::5] *= np.float32(2.0 ** 118)
+    x = synth.f32_to_bf16_bits(x)
+    c, s, z = weights(rng, N, K, group, zeros)
+    s *= np.float32(2.0 ** -30)
+    if zeros:
+        z[::2] = rng.integers(0, 256, z[::2].shape)
+    out = run(dev(x), c, s, z)
+    want, tol = step.int4_linear_ref(x, c, s, z)
+    f = quant.bf16_bits_to_f32(bits_of(out)).astype(np.float64)
+    assert np.isfinite(f).all()
+    assert (np.abs(f - want) <= np.abs(want) * 2.0 ** -8 + tol * (1 + 2.0 ** -8)).all()
+    # a result beyond the type is an infinity with its sign, a row with a NaN or infinity is NaN
+    s *= np.float32(2.0 ** 60)
+    x[-1, K - 1] = 0x7f80
+    f = quant.bf16_bits_to_f32(bits_of(run(dev(x), c, s, z))).astype(np.float64)
+    want, tol = (a[:-1] * 2.0 ** 60 for a in (want, tol))
+    far = np.abs(want) > 2.0 ** 129 + 2 * tol
+    assert np.array_equal(f[:-1][far], np.sign(want[far]) * np.inf) and np.isnan(f[-1]).all()
+    near = np.abs(want) < 2.0 ** 127 - 2 * tol
+    assert (np.abs(f[:-1] - want)[near] <= (np.abs(want) * 2.0 ** -8 + tol * (1 + 2.0 ** -8))[near]).all()
+
+
 @pytest.mark.parametrize("M, N, K", [(24, 515, 8192), (100, 300, 4096)])
 def test_workspaces(M, N, K):
     """A call without the workspace, or with a part of it, does not cut K."""
