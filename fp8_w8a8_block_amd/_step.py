@@ -315,7 +315,10 @@ def int4_linear(x, codes, scales, zeros=None, out=None, workspace=None):
 
 
 def logprobs_workspace_bytes(T, V, k=0, dtype=torch.bfloat16):
-    """Workspace bytes of token_logprobs for logits [T, V] of this type."""
+    """Workspace bytes of token_logprobs for logits [T, V] of this type.
+
+    Fewer rows may need more: a buffer for any count up to T has the largest
+    size over 1 .. min(T, 255) and T."""
     return _logprobs_workspace(_logits_type(dtype), int(T), int(V), int(k))
 
 

@@ -162,7 +162,10 @@ enum { FP8_LOGITS_BF16 = 0, FP8_LOGITS_F32 = 1 };
 #define FP8_MAX_TOP 64
 
 /* Bytes of workspace that fp8_token_logprobs needs (0 where a row's one workgroup
- * does all of it). */
+ * does all of it).  The size is that of these T rows, and fewer may need more: many
+ * rows of up to 4096 segments of 128 bytes need none, a few are cut into parts.  A buffer
+ * for any count up to T has the largest size over 1 .. min(T, 255) and T (from 256
+ * rows on it is 0 or grows with T). */
 size_t fp8_logprobs_workspace_bytes(int logits_type, int64_t T, int64_t V, int64_t k);
 
 /* fp8_token_logprobs -- what an answer's tokens were worth to the model.

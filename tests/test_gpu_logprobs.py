@@ -217,6 +217,19 @@ def test_smallest_scales(T, V, bf16):
         check(x, tokens, 9, scale=scale)
 
 
+@pytest.mark.parametrize("V, bf16", [(128000, True), (100003, False), (600000, True)])
+def test_one_workspace_for_a_falling_number_of_rows(V, bf16):
+    """Its size is not one of the largest batch: the largest over all row counts serves each."""
+    rng = np.random.default_rng(11)
+    x = logits(rng, 300, V, bf16)
+    tokens = rng.integers(0, V, 300)
+    n = max(fp8.logprobs_workspace_bytes(T, V, 3, x.dtype) for T in [*range(1, 257), 300])
+    store = torch.full((n + 64,), 0xff, dtype=torch.uint8, device="cuda")
+    for T in (300, 256, 255, 64, 1):
+        check(x[:T], tokens[:T], 3, workspace=store[16:16 + n])
+        assert (store[:16] == 0xff).all() and (store[16 + n:] == 0xff).all()
+
+
 def test_buffers_are_written_whole_and_nothing_else():
     rng = np.random.default_rng(6)
     T, V, k = 6, 90000, 3

@@ -227,6 +227,23 @@ def test_logprob_workspace_sizes():
     assert size(4096, 1 << 20) > 0                    # more segments than LDS holds
 
 
+def test_logprob_workspace_of_any_number_of_rows():
+    """What a buffer for up to T rows needs is the size's largest value over them: 0 or growing
+    from 256 rows on, so that of the first 255 and T."""
+    def size(T, V, kind):
+        return _step.lib().fp8_logprobs_workspace_bytes(kind, T, V, 1)
+
+    for kind in (0, 1):
+        for V in (1, 32000, 100003, 128000, 262145, 600000, 1 << 20, 5000000):
+            few = max(size(T, V, kind) for T in range(1, 256))
+            last = size(256, V, kind)
+            for T in [*range(257, 700, 13), *range(700, 5000, 331), 65536]:
+                n = size(T, V, kind)
+                assert n == last == 0 or n > last
+                last = n
+            assert V < 262145 or few > 0
+
+
 def test_binding_refuses_before_the_library():
     x = torch.zeros((2, 128), dtype=torch.bfloat16)
     w = torch.ones(128, dtype=torch.bfloat16)
