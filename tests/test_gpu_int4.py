@@ -186,6 +186,36 @@ def test_values_near_the_types_end(M, N, K, group, zeros):
     assert (np.abs(f[:-1] - want)[near] <= (np.abs(want) * 2.0 ** -8 + tol * (1 + 2.0 ** -8))[near]).all()
 
 
+@pytest.mark.parametrize("M", [1, 4, 13, 40, 150, 1000])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_each_place_finds_its_weight(M, group):
+    """Each place of two blocks of 128 values, as many of them a call as there are rows."""
+    K, N = 256, 80 if M < 1000 else 1100
+    rng = np.random.default_rng(M)
+    c, s, z = weights(rng, N, K, group, True)
+    s[:] = np.float32(0.25)
+    d = [torch.from_numpy(a).cuda() for a in (step.int4_pack_ref(c), s, z)]
+    want = (c.astype(int) - np.repeat(z, group, 1).astype(int)).T * 0.25
+    for k0 in range(0, K, M):
+        x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+        ks = torch.arange(k0, min(K, k0 + M), device="cuda")
+        x[torch.arange(len(ks), device="cuda"), ks] = 1.0
+        out = fp8.int4_linear(x, *d)[:len(ks)].float().cpu().numpy()
+        assert np.array_equal(out, want[k0:k0 + M]), k0
+
+
+@pytest.mark.parametrize("M, N, K", FAR)
+@pytest.mark.parametrize("group, zeros", [(32, False), (64, True), (128, True)])
+def test_subnormal_values(M, N, K, group, zeros):
+    """Subnormal values of x keep their part in both of the sums."""
+    rng = np.random.default_rng([M, N, group, 1])
+    x = rng.integers(0, 128, (M, K)).astype(np.uint16)
+    x |= (rng.integers(0, 2, (M, K)) << 15).astype(np.uint16)
+    c, s, z = weights(rng, N, K, group, zeros)
+    s *= np.float32(2.0 ** 100)
+    check(run(dev(x), c, s, z), x, c, s, z)
+
+
 @pytest.mark.parametrize("M, N, K", [(24, 515, 8192), (100, 300, 4096)])
 def test_workspaces(M, N, K):
     """A call without the workspace, or with a part of it, does not cut K."""

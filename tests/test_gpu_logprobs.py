@@ -225,9 +225,13 @@ def test_one_workspace_for_a_falling_number_of_rows(V, bf16):
     tokens = rng.integers(0, V, 300)
     n = max(fp8.logprobs_workspace_bytes(T, V, 3, x.dtype) for T in [*range(1, 257), 300])
     store = torch.full((n + 64,), 0xff, dtype=torch.uint8, device="cuda")
+    given = torch.as_tensor(tokens, device="cuda")
     for T in (300, 256, 255, 64, 1):
-        check(x[:T], tokens[:T], 3, workspace=store[16:16 + n])
+        got = fp8.token_logprobs(x[:T], given[:T], k=3, workspace=store[16:16 + n])
+        want = fp8.token_logprobs(x[:T], given[:T], k=3)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert (store[:16] == 0xff).all() and (store[16 + n:] == 0xff).all()
+    check(x[:3], tokens[:3], 3, workspace=store[16:16 + n])
 
 
 def test_buffers_are_written_whole_and_nothing_else():

@@ -390,6 +390,27 @@ def test_int4_of_a_large_weight(case):
     tail_products(x, codes, scales, zeros, out, rows)
 
 
+def test_int4_pack_and_quantization_of_large_weights():
+    """Packed codes past 4 GiB: the rows there are the ones they are alone."""
+    N, K = 33000, 2 ** 18 + 128
+    assert N * K // 2 > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(2)
+    values = torch.empty((N, K), dtype=torch.uint8, device="cuda").random_(generator=g)
+    codes = fp8.int4_pack(values)
+    parts = [slice(0, 2), slice(N // 2, N // 2 + 2), slice(N - 2, N)]
+    for rows in parts:
+        assert np.array_equal(codes[rows].cpu().numpy(), step.int4_pack_ref(values[rows].cpu().numpy() & 15))
+    del values, codes
+    w = torch.empty((N, K), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    for group, symmetric in ((32, False), (128, True)):
+        codes, scales, zeros = fp8.int4_quant_weight(w, group, symmetric)
+        for rows in parts:
+            c, s, z = step.int4_quant_ref(bits_of(w[rows]), group, symmetric)
+            assert np.array_equal(codes[rows].cpu().numpy(), step.int4_pack_ref(c))
+            assert np.array_equal(scales[rows].cpu().numpy().view(np.uint32), s.view(np.uint32))
+            assert zeros is None if symmetric else np.array_equal(zeros[rows].cpu().numpy(), z)
+
+
 def test_int4_rows_far_apart():
     rng, N, K = np.random.default_rng(9), 200, 256
     w = fp8.int4_quant_weight(bf16(rng.standard_normal((N, K))), 32)
