@@ -157,6 +157,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, uint32_t
   const StaticDivisor kd = make_static_divisor(a.k_scale[0]);
   const StaticDivisor vd = make_static_divisor(a.v_scale[0]);
   const float inv_d = 1.0f / (float)a.D;
+  const float least = a.eps < 0x1p-100f ? 0x1p-80f : 0.0f;   // smaller sums may have lost squares
 
   for (int h = h0; h < heads; h += (int)chunks) {
     const uint4 x = next;
@@ -179,7 +180,20 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, uint32_t
     }
 #pragma unroll
     for (int m = 1; m < L; m <<= 1) ss += __shfl_xor(ss, m);
-    const float r = rsqrt_of(__builtin_fmaf(ss, inv_d, a.eps));
+    float r = rsqrt_of(__builtin_fmaf(ss, inv_d, a.eps));
+    if (__ballot(__builtin_amdgcn_fmed3f(ss, least, 0x1p+126f) != ss)) {
+      // A head of the wave has squares that leave fp32's range.  Those of f x do not; f
+      // stays with small x, whose 1 / rms may be beyond it.  (The test costs about 1 %.)
+      const float f = ss > 0x1p+126f ? 0x1p-80f : ss < least ? 0x1p+90f : 1.0f;
+      ss = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(y[e] * f, y[e] * f, ss);
+#pragma unroll
+      for (int m = 1; m < L; m <<= 1) ss += __shfl_xor(ss, m);
+      r = rsqrt_of(__builtin_fmaf(ss, inv_d, a.eps * f * f)) * (f > 1.0f ? 1.0f : f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= f > 1.0f ? f : 1.0f;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       y[e] = y[e] * r * ((e & 1) ? bf16_hi(ww[e / 2]) : bf16_lo(ww[e / 2]));

@@ -78,8 +78,9 @@ fp8_status fp8_kv_slot_map(const int32_t* computed_lens, const int32_t* new_lens
  *   (y_a, y_b) -> (y_a c_i - y_b s_i, y_b c_i + y_a s_i)   for i < rot_dim / 2
  * with (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved is
  * nonzero; elements from rot_dim on are only normalized.  Computed in fp32
- * and rounded once: queries to bf16 (round to nearest even; a NaN gives a
- * quiet NaN), keys to E4M3(y / k_scale), values to E4M3(v / v_scale), bit for bit as
+ * (finite values of any size keep their mean of squares) and rounded once:
+ * queries to bf16 (round to nearest even; a NaN gives a quiet NaN), keys to
+ * E4M3(y / k_scale), values to E4M3(v / v_scale), bit for bit as
  * fp8_kv_cache_write stores them.  A token whose position is outside
  * [0, max_pos) is padding: nothing of it is written.  A slot outside the
  * cache is not stored, its query is written.  Two tokens with one slot leave

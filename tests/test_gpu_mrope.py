@@ -141,6 +141,41 @@ def test_one_position_on_all_axes_is_the_plain_call(inter):
         assert np.array_equal(g[2], vc.cpu().numpy())
 
 
+@pytest.mark.parametrize("sections, inter", [((64,), False), ((24, 20, 20), False), ((24, 20, 20), True)])
+def test_heads_whose_squares_leave_the_range(sections, inter):
+    """Heads of values whose squares overflow or vanish in fp32, next to ordinary ones; without eps."""
+    rng = np.random.default_rng(11)
+    T, Hq, Hk, D = 24, 6, 3, 128
+    d = inputs(12, T, Hq, Hk, D, D, 16, len(sections))
+    x = rng.standard_normal((T, Hq + 2 * Hk, D))
+    scale = 2.0 ** rng.choice([0, 55, 64, 90, 120, -38, -60, -80, -120, -128], x.shape[:2])
+    scale[0] = 1.0
+    x[1, :, 0], x[1, :, 1:] = 1.5, 0                            # one value alone
+    d["row"] = synth.f32_to_bf16_bits((x * scale[..., None]).astype(np.float32))
+    d["row"][2, :, 5] = synth.f32_to_bf16_bits(np.float32(3.0))
+    row = dev(d["row"])
+    kc, vc = (torch.from_numpy(d[n].copy()).cuda() for n in ("k0", "v0"))
+    got = fp8.qk_norm_mrope_cache(
+        row[:, :Hq], row[:, Hq:Hq + Hk], row[:, Hq + Hk:], dev(d["qw"]), dev(d["kw"]),
+        torch.from_numpy(d["cs"]).cuda(), torch.from_numpy(d["pos"]).cuda(), sections,
+        torch.from_numpy(d["slots"]).cuda(), kc, vc, torch.tensor([KS], device="cuda"),
+        torch.tensor([VS], device="cuda"), eps=0.0, in_turn=len(sections) > 1, interleaved=inter)
+    torch.cuda.synchronize()
+    axis = np.array(step.axes_ref(sections, len(sections) > 1))
+    half, pos = np.arange(D // 2), d["pos"][axis].T
+    cos, sin = (d["cs"][pos, half + i].astype(np.float64) for i in (0, D // 2))
+    x = quant.bf16_bits_to_f32(d["row"]).astype(np.float64)
+    qw, kw = (quant.bf16_bits_to_f32(d[n]).astype(np.float64) for n in ("qw", "kw"))
+    z, tol = attention.norm_rope_ref(x[:, :Hq], qw, 0.0, cos, sin, inter)
+    f = quant.bf16_bits_to_f32(bits_of(got)).astype(np.float64)
+    assert (np.abs(f - z) <= np.abs(z) * 2.0 ** -8 + tol * 2).all()
+    z, tol = attention.norm_rope_ref(x[:, Hq:Hq + Hk], kw, 0.0, cos, sin, inter)
+    lo, hi = ((z + s * (tol + np.abs(z) * 2.0 ** -23)) / np.float64(KS) for s in (-1, 1))
+    lo, hi = (e4m3.decode(e4m3.encode(v.astype(np.float32))).astype(np.float64) for v in (lo, hi))
+    v = e4m3.decode(kc.cpu().numpy().reshape(-1, Hk, D)[d["slots"]]).astype(np.float64)
+    assert ((v >= lo) & (v <= hi)).all()
+
+
 def test_refusals():
     d = inputs(5, 4, 2, 1, 64, 64, 16, 3)
     x, w, one = dev(d["row"]), dev(d["qw"]), torch.ones(1, device="cuda")
