@@ -9,7 +9,7 @@
 // 16 neighbouring lanes hold a 128-group, whose maximum is a DPP reduction.
 // 8191 rows of 4096 with codes by groups (236 MB) take 44 us, 5.4 TB/s, where a copy
 // of 2 GiB moves 4.9; 2049 of 7168 with the bf16 norm and codes by rows (132 MB) 24 to
-// 28 us; 4 rows 3.1 us, the way through two loads, a sum across waves and a store.
+// 29 us; 4 rows 3.1 us, the way through two loads, a sum across waves and a store.
 #include "device_common.h"
 #include "fp8w8a8.h"
 #include "step_launch.h"
@@ -129,8 +129,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_quant_kernel(NormQ
     ss = row_sum<W>(squares(f), red_again);
   }
   // v = (r up) rs weight: 1 / rms of a row that small may be beyond fp32, so f stays with r.
-  // (One product more a value, 0.5 % of the time of 8191 rows of 4096; a branch around it,
-  // or the row made larger in its registers, spills where 16 waves hold 8 chunks a lane.)
+  // (One product more a value, under 1 % of the time of 8191 rows of 4096; a branch around
+  // it, or the row made larger in its registers, spills where 16 waves hold 8 chunks a lane:
+  // 104 and 77 us for 500 rows of 65536 with codes by rows, 45 like this.)
   const float up = f > 1.0f ? f : 1.0f;
   const float rs = rsqrt_of(__builtin_fmaf(ss, inv_h, a.eps * f * f)) * (f > 1.0f ? 1.0f : f);
 
@@ -214,6 +215,8 @@ void launch_wc(const NormQuantArgs& a, int mode, hipStream_t st) {
 // two, 6.1 / 48.2 with one of eight; H 7168 3.8 / 73.1 with eight of two, 4.4 / 75.6
 // with four of four; H 16384 4.9 / 166.5 with sixteen of two, 6.8 / 164.7 with four
 // of eight; H 32768 8.1 / 359 with sixteen of four, 8.4 / 357 with eight of eight.
+// H 65536 13.0 / 764 (4.9 TB/s) with sixteen of eight, which spill 8 registers without
+// codes (8.9 / 810) and 2 with codes by rows (11.8 / 740).
 hipError_t launch_norm_quant(const NormQuantArgs& a, int mode, hipStream_t st) {
   const int chunks = a.H / 8;
   if (chunks <= 64)

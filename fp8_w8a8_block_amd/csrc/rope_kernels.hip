@@ -14,8 +14,8 @@
 // has the next head's load in flight while it works on one.  8191 tokens of 32
 // + 8 + 8 heads of 128 (189 MB) take 42 us, 4.5 TB/s, where a large copy moves
 // 4.85; more loads in flight per lane (2, 4, 8 heads) cost occupancy and time
-// (44, 47, 65 us).  With positions on three axes they take 44.7 us where the one-axis
-// call takes 40.3: two more positions and four more reads of angles per lane group.
+// (44, 47, 65 us).  With positions on three axes they take 45.1 us where the one-axis
+// call takes 40.7: two more positions and four more reads of angles per lane group.
 #include "attention_launch.h"
 #include "device_common.h"
 #include "launch.h"
@@ -183,7 +183,8 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeArgs a, uint32_t
     float r = rsqrt_of(__builtin_fmaf(ss, inv_d, a.eps));
     if (__ballot(__builtin_amdgcn_fmed3f(ss, least, 0x1p+126f) != ss)) {
       // A head of the wave has squares that leave fp32's range.  Those of f x do not; f
-      // stays with small x, whose 1 / rms may be beyond it.  (The test costs about 1 %.)
+      // stays with small x, whose 1 / rms may be beyond it.  (The test costs 0.5 to
+      // 1 %: 40.3 and 40.7 us, 44.9 and 45.1 with three axes.)
       const float f = ss > 0x1p+126f ? 0x1p-80f : ss < least ? 0x1p+90f : 1.0f;
       ss = 0.0f;
 #pragma unroll

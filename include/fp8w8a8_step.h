@@ -78,7 +78,7 @@ enum { FP8_AXES_SECTIONS = 0, FP8_AXES_IN_TURN = 1 };
  *             FP8_AXES_IN_TURN: pair i belongs to axis a = i % A while
  *             i < A * sections[a], else to axis 0; sections of the axes from 1
  *             on must fit, a + A * (sections[a] - 1) < rot_dim / 2
- * 1 <= A <= 4.  All else as for fp8_qk_norm_rope_cache; a token with a position
+ * 1 <= A <= 4; ld_pos >= T where A > 1.  All else as for fp8_qk_norm_rope_cache; a token with a position
  * outside [0, max_pos) on any axis is padding, also where that axis turns no
  * pair.  With one axis the results are that call's, bit for bit. */
 fp8_status fp8_qk_norm_mrope_cache(
@@ -137,7 +137,9 @@ size_t fp8_int4_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * The matrix unit multiplies bf16 x with the exact integers 16 + code; the sums
  * of a group are fp32, 16 + zero times the group's sum of x is taken off in
  * fp32, and the scaled groups are summed in fp32.  Nothing is rounded below
- * that but the result.  Where a sum leaves fp32's range on the way (|x| from
+ * that but the result; where c - z is small the offset's part of the sums makes
+ * their rounding up to (16 + c) / |c - z| times as large, and a far value of x with
+ * c = z leaves what its products were rounded by.  Where a sum leaves fp32's range on the way (|x| from
  * about 2^112 on), the result is formed again in 64 bits, by a few lanes: right, but
  * slow.  A row of x that holds an infinity or a NaN gives NaN.
  * group 32, 64 or 128; K a positive multiple of 128 below 2^24; any N >= 1 and
@@ -149,7 +151,7 @@ size_t fp8_int4_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * runs of K that it counts are summed in fp32 by workgroups of their own and
  * then added, in order: the same arithmetic, so results can differ from the
  * uncut call's in the last bits.  A smaller or NULL workspace runs the call
- * uncut. */
+ * uncut.  A row's last bits can depend on M, too, which chooses tiles and runs. */
 fp8_status fp8_int4_linear(const uint16_t* x, int64_t ld_x, const uint8_t* codes,
                            const float* scales, const uint8_t* zeros, int64_t group, uint16_t* out,
                            int64_t ld_out, int64_t M, int64_t N, int64_t K, void* workspace,
@@ -179,7 +181,8 @@ size_t fp8_logprobs_workspace_bytes(int logits_type, int64_t T, int64_t V, int64
  *   top_logprobs [T, k] fp32, top_ids [T, k] int32, contiguous: the k largest
  *            z - lse, in falling order, of equal logits the lower index first;
  *            both NULL if k is 0                                          (output)
- * One pass over the logits, sums in fp32.  A logit of -inf has probability 0: its log
+ * One pass over the logits, sums in fp32, in an order that T, V and the row's place
+ * in memory choose: last bits can depend on them.  A logit of -inf has probability 0: its log
  * probability is -inf, and it comes among the alternatives after all others.  A log
  * probability below fp32's range is -inf, too, and an lse beyond it an infinity,
  * beside log probabilities as they are.
